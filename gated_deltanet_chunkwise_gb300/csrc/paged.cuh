@@ -72,24 +72,32 @@ struct PagedAttnParams {
   int* status;
 };
 
-// new tokens [q0, q0 + len) of a sequence and its keys; ok false (recorded)
-// when the lengths are inconsistent with the batch or the page table.
+// New tokens [q0, q0 + len) of a sequence and its keys; ok false (recorded)
+// when the lengths are inconsistent with the batch or the page table, ordered
+// false when it is the batch's offsets that decrease or leave it.
 struct PagedSeq {
   int q0, len, kv;
-  bool ok;
+  bool ok, ordered;
 };
+
+// Offsets of a packed batch that do not decrease and stay inside of it: checked
+// pair by pair. (Both attention kernels look at all pairs and write nothing if
+// one is wrong: how sequences that overlap share rows has no answer.)
+__device__ __forceinline__ bool ordered_pair(int b, int e, int T) {
+  return b >= 0 && e >= b && e <= T;
+}
 
 __device__ __forceinline__ PagedSeq paged_seq(const PagedView& c,
                                               const int32_t* cu, int T, int n,
                                               int* status) {
   PagedSeq s;
   s.kv = c.kv_lens[n];
-  s.ok = true;
+  s.ok = s.ordered = true;
   if (cu) {
     const int b = cu[n], e = cu[n + 1];
     s.q0 = b;
     s.len = e - b;
-    if (b < 0 || e < b || e > T) s.ok = false;
+    s.ok = s.ordered = ordered_pair(b, e, T);
   } else {
     s.q0 = n * T;
     s.len = T;

@@ -56,6 +56,11 @@ __global__ void __launch_bounds__(kThreads)
                         warp / warps_per_token;
   tc::griddep_launch_dependents();
   tc::griddep_wait();
+  // offsets that decrease or leave the batch, which a token may not meet
+  if (p.cu && blockIdx.x == 0)
+    for (int j = threadIdx.x; j < p.N; j += kThreads)
+      if (!ordered_pair(p.cu[j], p.cu[j + 1], p.T))
+        record_status(p.status, GDN_ERR_INVALID_ARG);
   if (tok >= p.tokens) return;
   int n;
   if (p.cu) {
@@ -68,7 +73,10 @@ __global__ void __launch_bounds__(kThreads)
   if (!s.ok) return;
   const int i = (int)tok - s.q0;
   const int x = s.kv - s.len + i;
-  if (i < 0 || i >= s.len || x < 0) {
+  // before the first sequence: belongs to none (or between offsets that
+  // decrease, recorded above)
+  if (i < 0 || i >= s.len) return;
+  if (x < 0) {
     record_status(p.status, GDN_ERR_INVALID_ARG);
     return;
   }

@@ -72,6 +72,7 @@ struct Seq {
   int q0, len, kv;
   int tile0, tiles;  // key tiles [tile0, tile0 + tiles)
   int blocks;        // row blocks
+  bool ordered;      // its offsets in a packed batch are
 };
 
 __device__ __forceinline__ Seq seq_work(const PagedAttnParams& p, int n) {
@@ -80,6 +81,7 @@ __device__ __forceinline__ Seq seq_work(const PagedAttnParams& p, int n) {
   w.q0 = s.q0;
   w.len = s.len;
   w.kv = s.kv;
+  w.ordered = s.ordered;
   const long long n_rows = (long long)s.len * p.group;
   w.blocks = n_rows <= p.rows_max ? (int)((n_rows + ROWS - 1) / ROWS) : 0;
   int lo = 0;
@@ -302,7 +304,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   const int per_t = (p.N + kThreads - 1) / kThreads;
   const int n_lo = min(p.N, tid * per_t), n_hi = min(p.N, n_lo + per_t);
   long long mine = 0;
-  for (int n = n_lo; n < n_hi; ++n) mine += seq_units<SPLIT>(p, seq_work(p, n));
+  bool bad = false;
+  for (int n = n_lo; n < n_hi; ++n) {
+    const Seq s = seq_work(p, n);
+    mine += seq_units<SPLIT>(p, s);
+    bad = bad || !s.ordered;
+  }
   long long scan = mine;
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) {
@@ -310,15 +317,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (lane >= o) scan += up;
   }
   if (lane == 31) s_sum[warp] = scan;
-  __syncthreads();
+  const bool skip = __syncthreads_or(bad);
   long long total = 0, before = scan - mine;
 #pragma unroll
   for (int i = 0; i < kThreads / 32; ++i) {
     if (i < warp) before += s_sum[i];
     total += s_sum[i];
   }
-  // (a split call has a block for every part; units past the blocks are those
-  // of sequences that overlap, which other blocks serve)
+  if (skip) total = 0;
+  // (a split call has a block for every part)
   const long long per =
       SPLIT ? 1 : (total + gridDim.x - 1) / gridDim.x;
   Walk walk;

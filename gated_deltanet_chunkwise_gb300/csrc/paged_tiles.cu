@@ -207,7 +207,8 @@ __device__ __forceinline__ void step(const PagedAttnParams& p, Place& x,
 
 __device__ __forceinline__ Slot slot_at(const PagedAttnParams& p,
                                         const Place& x, int tt) {
-  return slot_work(p, x.n, max(0, x.slot - x.first), tt);
+  // (negative where tokens before the first sequence would be: no rows)
+  return slot_work(p, x.n, x.slot - x.first, tt);
 }
 
 // Units of the list that a slot takes: each head's item counts its key tiles
@@ -453,19 +454,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   // later) while the run's place is sought: one trip to memory instead of one
   // per probe.
   PagedAttnParams ps = p;
-  if (p.N <= kLengthsStaged) {
-    int32_t* lens = reinterpret_cast<int32_t*>(sm_kv);
-    int32_t* cu = lens + kLengthsStaged;
+  const bool staged = p.N <= kLengthsStaged;
+  int32_t* lens = reinterpret_cast<int32_t*>(sm_kv);
+  int32_t* cu = lens + kLengthsStaged;
+  if (staged)
     for (int i = tid; i < p.N; i += kThreads) lens[i] = p.c.kv_lens[i];
-    if (p.cu)
-      for (int i = tid; i <= p.N; i += kThreads) cu[i] = p.cu[i];
-    __syncthreads();
+  bool bad = false;
+  if (p.cu)
+    for (int i = tid; i < p.N; i += kThreads) {
+      const int b = p.cu[i], e = p.cu[i + 1];
+      bad = bad || !ordered_pair(b, e, p.T);
+      if (staged) {
+        cu[i] = b;
+        if (i + 1 == p.N) cu[p.N] = e;
+      }
+    }
+  if (bad) record_status(p.status, GDN_ERR_INVALID_ARG);
+  const bool skip = __syncthreads_or(bad);
+  if (staged) {
     ps.c.kv_lens = lens;
     if (p.cu) ps.cu = cu;
   }
 
-  // where this CTA's run lies: thread t sums slots [t * per_t, ...)
-  const int slots = slot_count(p, tt);
+  // where this CTA's run lies: thread t sums slots [t * per_t, ...). (The slots
+  // of a packed batch follow its offsets, so they have to be in order.)
+  const int slots = skip ? 0 : slot_count(p, tt);
   const int per_t = (slots + kThreads - 1) / kThreads;
   const int lo_s = (int)min((long long)slots, (long long)tid * per_t);
   const int hi_s = min(slots, lo_s + per_t);

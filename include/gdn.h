@@ -461,14 +461,17 @@ typedef struct {
  *               pairs each axis turns, summing to rot/2 (ignored, and may be
  *               NULL, with axes = 1)
  *   cu_seqlens  NULL: a dense batch of B sequences with T new tokens each.
- *               Device int32 [B + 1]: packed, tensors [1, T, H, d]; sequences
- *               may be empty, and tokens from cu_seqlens[B] on belong to none
- *               and are left alone
+ *               Device int32 [B + 1]: packed, tensors [1, T, H, d]; offsets
+ *               in [0, T] that do not decrease. Sequences may be empty, and
+ *               tokens before cu_seqlens[0] or from cu_seqlens[B] on belong to
+ *               none and are left alone
  * New token i of sequence n goes to place kv_lens[n] - new_n + i. Tokens whose
  * place is negative or past the table, whose page is not in [0, num_pages) or
  * whose position is not in [0, rope_rows) are left out, and
- * GDN_ERR_INVALID_ARG is recorded (gdn_device_status). Places must differ: two
- * tokens sent to one slot of a page race.
+ * GDN_ERR_INVALID_ARG is recorded (gdn_device_status); it is recorded, too,
+ * where offsets decrease or leave [0, T], and the tokens of such a sequence are
+ * left out (which of the others are appended is then not specified). Places
+ * must differ: two tokens sent to one slot of a page race.
  * Arithmetic is fp32, rounded once to the 16-bit type. One launch, no
  * workspace.
  */
@@ -512,10 +515,10 @@ int gdn_paged_append(const void* q, int64_t q_stride, const void* k,
  * or not, and an infinity or a NaN among a sequence's own keys and values
  * reaches the tokens that see it and no others. Scores, maxima, sums and
  * accumulators are fp32; weights are rounded to the 16-bit type for their
- * product with V, and the output once. A sequence whose lengths do not fit the
- * batch or the table is skipped (its rows are not written) and a page outside
- * the pool reads as zeros; both record GDN_ERR_INVALID_ARG. Results do not
- * depend on timing.
+ * product with V, and the output once. A sequence whose keys do not fit the
+ * table is skipped (its rows are not written), offsets that decrease or leave
+ * [0, T] leave every row unwritten, and a page outside the pool reads as zeros;
+ * all three record GDN_ERR_INVALID_ARG. Results do not depend on timing.
  * Workspace: none (a table of few pages), 5 MB (few rows) or up to 41 MB per
  * call in flight, stream-ordered, from a memory pool of the library's own on
  * the device that keeps what it has been given (the device's default pool would
