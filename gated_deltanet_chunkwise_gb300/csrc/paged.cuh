@@ -194,6 +194,16 @@ __device__ __forceinline__ void wait_out_copies() {
   }
 }
 
+// Hidden values. The products that the kernels make of whole tiles multiply the
+// values of keys that a row does not see by a weight of 0, which an infinity or
+// a NaN among them survives. A CTA that finds a result which is not finite in a
+// row that does not see all that was multiplied makes its run once more, with a
+// look through the tiles that some row sees in part: if one holds such a value,
+// its weights are multiplied key by key, each row's with the keys that it sees
+// and no others. So ordinary calls pay for a look at their results only; one
+// hidden infinity makes 2048 tokens over 65536 keys take 2.4 ms instead of 0.7,
+// and the cost of a tile made key by key does not grow with the cache.
+
 // 1 if any of the values is infinite or NaN.
 __device__ __forceinline__ uint32_t nonfinite(const float (&x)[32]) {
   float z[2] = {};
@@ -202,72 +212,26 @@ __device__ __forceinline__ uint32_t nonfinite(const float (&x)[32]) {
   return z[0] + z[1] == 0.f ? 0u : 1u;
 }
 
-// Columns [col, col + 32) of one row's unnormalised output over keys [k0, k1)
-// of sequence n, one thread, straight from the definition. The products that
-// the kernels make of whole tiles multiply the values of keys that a row does
-// not see by a weight of 0, which an infinity or a NaN among them survives; a
-// row whose result is not finite is therefore summed once more here, over the
-// keys that it sees and no others. (A row that does see such a value stays
-// what it is. Slow, some microseconds a key, but it ends once every column is
-// NaN: where all is NaN, at once.)
-template <typename E, int D>
-__device__ __noinline__ void exact_columns(const PagedAttnParams& p, int n,
-                                           int head, const E* q, int k0, int k1,
-                                           float ref, int col, float* out) {
-  float acc[32];
-#pragma unroll
-  for (int e = 0; e < 32; ++e) acc[e] = 0.f;
-  const float m = ref == kNegInf ? 0.f : ref;
-  for (int key = k0; key < k1; ++key) {
-    const int pid = p.c.table[(long long)n * p.c.table_stride +
-                              (key >> p.c.page_shift)];
-    const int slot = key & ((1 << p.c.page_shift) - 1);
-    float s[4] = {};
-    const bool held = pid >= 0 && pid < p.c.num_pages;  // else reads as zeros
-    if (held) {
-      const E* k = static_cast<const E*>(p.c.k) + pid * p.c.k_page +
-                   head * p.c.k_head + slot * p.c.k_token;
-#pragma unroll
-      for (int e = 0; e < D; e += 8) {
-        const uint4 a = *reinterpret_cast<const uint4*>(q + e);
-        const uint4 b = *reinterpret_cast<const uint4*>(k + e);
-        const uint32_t ua[4] = {a.x, a.y, a.z, a.w}, ub[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 x = unpack2(ua[i], E()), y = unpack2(ub[i], E());
-          s[i] = fmaf(x.x, y.x, fmaf(x.y, y.y, s[i]));
-        }
-      }
-    }
-    const float w =
-        ex2(((s[0] + s[1]) + (s[2] + s[3])) * p.scale_log2 - m);
-    bool all = w != w;
-    if (held) {
-      const E* v = static_cast<const E*>(p.c.v) + pid * p.c.v_page +
-                   head * p.c.v_head + slot * p.c.v_token + col;
-      bool every = true;
-#pragma unroll
-      for (int e = 0; e < 32; e += 8) {
-        const uint4 b = *reinterpret_cast<const uint4*>(v + e);
-        const uint32_t ub[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 y = unpack2(ub[i], E());
-          acc[e + 2 * i] = fmaf(w, y.x, acc[e + 2 * i]);
-          acc[e + 2 * i + 1] = fmaf(w, y.y, acc[e + 2 * i + 1]);
-          every = every && acc[e + 2 * i] != acc[e + 2 * i] &&
-                  acc[e + 2 * i + 1] != acc[e + 2 * i + 1];
-        }
-      }
-      all = all || every;
-    } else if (all) {
-#pragma unroll
-      for (int e = 0; e < 32; ++e) acc[e] = w;
-    }
-    if (all) break;
-  }
-#pragma unroll
-  for (int e = 0; e < 32; ++e) out[e] = acc[e];
+// (0, 0), of either sign, as long as all the elements seen are finite.
+__device__ __forceinline__ uint32_t probe2(uint32_t u, uint32_t acc, __nv_bfloat16) {
+  const __nv_bfloat162 z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u),
+                                   __floats2bfloat162_rn(0.f, 0.f),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&acc));
+  return *reinterpret_cast<const uint32_t*>(&z);
+}
+__device__ __forceinline__ uint32_t probe2(uint32_t u, uint32_t acc, __half) {
+  const __half2 z = __hfma2(*reinterpret_cast<const __half2*>(&u),
+                            __floats2half2_rn(0.f, 0.f),
+                            *reinterpret_cast<const __half2*>(&acc));
+  return *reinterpret_cast<const uint32_t*>(&z);
+}
+template <typename E>
+__device__ __forceinline__ uint32_t probe8(uint4 v, uint32_t acc) {
+  return probe2(v.w, probe2(v.z, probe2(v.y, probe2(v.x, acc, E()), E()), E()),
+                E());
+}
+__device__ __forceinline__ bool probe_hit(uint32_t acc) {
+  return (acc & 0x7fff7fffu) != 0;
 }
 
 // ---- host side ------------------------------------------------------------------

@@ -63,8 +63,18 @@ struct Shape {
   // 96 KB in flight per CTA, two CTAs per SM
   static constexpr int kStages = 96 * 1024 / (2 * kTile);
   static constexpr int kRed = ROWS * D * 4;
-  static constexpr int kMisc = 1024;
+  static constexpr int kMisc = 4 * kStages * 8;  // barriers, for two passes
   static constexpr int kSmem = 1024 + kStages * 2 * kTile + kRed + kMisc;
+  // [kStages] full, [kStages] empty; the same for a second pass
+  static __device__ __forceinline__ uint64_t* barriers(char* sm) {
+    return reinterpret_cast<uint64_t*>(sm + kStages * 2 * kTile + kRed);
+  }
+  static __device__ __forceinline__ void init(uint64_t* bars) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bars[s], 1);
+      mbar_init(&bars[kStages + s], kConsumers);
+    }
+  }
 };
 
 // ---- the work list -------------------------------------------------------------
@@ -265,92 +275,32 @@ __device__ __noinline__ void join_cluster(const PagedAttnParams& p, const Seq& s
   }
 }
 
-template <typename E, int D, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
-    paged_rows_kernel(const __grid_constant__ PagedAttnParams p,
-                      const __grid_constant__ CUtensorMap tk,
-                      const __grid_constant__ CUtensorMap tv, int box) {
+// What the warps of a CTA share beside the tiles.
+struct Shared {
+  float m[kConsumers][ROWS], l[kConsumers][ROWS];  // warps' maxima and sums
+  float M[ROWS], L[ROWS];                          // the item's
+  long long sum[kThreads / 32];
+  long long base, total;  // first unit of sequence n, where the run begins; units
+  long long per;          // units of a run
+  int n, abort;
+  int redo;               // a result may hold what its row does not see
+};
+
+// A CTA's run. CAREFUL: with a look through the values of tiles that some row
+// sees in part. Leaves the last segment in g and its sequence in walk.
+template <typename E, int D, bool SPLIT, bool CAREFUL>
+__device__ __forceinline__ void serve(const PagedAttnParams& p,
+                                      const CUtensorMap& tk,
+                                      const CUtensorMap& tv, int box,
+                                      char* sm, Shared& c, Walk& walk,
+                                      Segment& g) {
   using S = Shape<D>;
   constexpr int KS = D / 16;
-  extern __shared__ char smem_raw[];
-  char* sm = reinterpret_cast<char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  float* red = reinterpret_cast<float*>(sm + S::kStages * 2 * S::kTile);
-  char* misc = sm + S::kStages * 2 * S::kTile + S::kRed;
-  uint64_t* full = reinterpret_cast<uint64_t*>(misc);
-  uint64_t* empty = full + S::kStages;
-  float* s_m = reinterpret_cast<float*>(misc + 256);  // [kConsumers][ROWS]
-  __shared__ float s_l[kConsumers][ROWS];
-  __shared__ float s_M[ROWS], s_L[ROWS];
-  __shared__ long long s_sum[kThreads / 32];
-  __shared__ long long s_base;
-  __shared__ int s_n, s_abort;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  volatile int* abort_flag = &s_abort;
-  if (tid == 0) {
-    s_abort = 0;
-    s_n = p.N;
-    for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kConsumers);
-    }
-    fence_mbar_init();
-    prefetch_tmap(&tk);
-    prefetch_tmap(&tv);
-  }
-  griddep_wait();  // nothing above touches what earlier kernels write
-
-  // where this CTA's run lies: thread t sums the sequences [t * per, ...)
-  const int per_t = (p.N + kThreads - 1) / kThreads;
-  const int n_lo = min(p.N, tid * per_t), n_hi = min(p.N, n_lo + per_t);
-  long long mine = 0;
-  bool bad = false;
-  for (int n = n_lo; n < n_hi; ++n) {
-    const Seq s = seq_work(p, n);
-    mine += seq_units<SPLIT>(p, s);
-    bad = bad || !s.ordered;
-  }
-  long long scan = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const long long up = __shfl_up_sync(0xffffffffu, scan, o);
-    if (lane >= o) scan += up;
-  }
-  if (lane == 31) s_sum[warp] = scan;
-  const bool skip = __syncthreads_or(bad);
-  long long total = 0, before = scan - mine;
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < warp) before += s_sum[i];
-    total += s_sum[i];
-  }
-  if (skip) total = 0;
-  // (a split call has a block for every part)
-  const long long per =
-      SPLIT ? 1 : (total + gridDim.x - 1) / gridDim.x;
-  Walk walk;
-  walk.w = per * blockIdx.x;
-  walk.w_end = walk.w + per < total ? walk.w + per : total;
-  if (walk.w < walk.w_end && mine > 0 && walk.w >= before &&
-      walk.w < before + mine) {
-    long long base = before;
-    int n = n_lo;
-    for (; n < n_hi; ++n) {
-      const long long u = seq_units<SPLIT>(p, seq_work(p, n));
-      if (walk.w < base + u) break;
-      base += u;
-    }
-    s_n = n;
-    s_base = base;
-  }
-  __syncthreads();
-  walk.n = s_n;
-  walk.base = s_base;
-  if (tid == 0 && !SPLIT) p.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
-  if (walk.n >= p.N) return;  // no work for this CTA
-  walk.s = seq_work(p, walk.n);
-
-  Segment g;
+  float* const red = reinterpret_cast<float*>(sm + S::kStages * 2 * S::kTile);
+  uint64_t* const full = S::barriers(sm) + (CAREFUL ? 2 * S::kStages : 0);
+  uint64_t* const empty = full + S::kStages;
+  volatile int* const abort_flag = &c.abort;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (warp == kConsumers) {
     // ---- producer ------------------------------------------------------------
     const int page = 1 << p.c.page_shift;
@@ -525,13 +475,54 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 sum[h] += a + b;
                 pf[2 * j + h] = pack2<E>(a, b);
               }
+          bool by_key = false;
+          if (CAREFUL && masked) {
+            // look through the values of the warp's keys
+            uint32_t z = 0;
+            for (int i = lane; i < 16 * (D / 8); i += 32)
+              z = probe8<E>(*reinterpret_cast<const uint4*>(
+                                vs_ + tile_off(kb + i / (D / 8), i % (D / 8))),
+                            z);
+            by_key = __any_sync(0xffffffffu, probe_hit(z));
+          }
+          if (by_key) {
+#pragma unroll 1
+            for (int key = 0; key < 16; ++key) {
+              const int from = (lane & ~3) | (key >> 1 & 3);
+              float w[2];
+              bool sees[2];
 #pragma unroll
-          for (int j = 0; j < D / 16; ++j) {
-            uint32_t bfr[4];
-            ldsm4_t(va + tile_off(kb + (mat & 1) * 8 + r8, 2 * j + (mat >> 1)),
-                    bfr);
+              for (int h = 0; h < 2; ++h) {
+                const float2 x = unpack2(
+                    __shfl_sync(0xffffffffu, key < 8 ? pf[h] : pf[2 + h], from),
+                    E());
+                w[h] = key & 1 ? x.y : x.x;
+                sees[h] = key0 + key < hi[h] && key0 + key >= lo[h];
+              }
+#pragma unroll
+              for (int j = 0; j < D / 8; ++j) {
+                const float2 x = unpack2(
+                    *reinterpret_cast<const uint32_t*>(
+                        vs_ + tile_off(kb + key, j) + t4 * 4),
+                    E());
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  if (sees[h]) {
+                    acc[j][2 * h] = fmaf(w[h], x.x, acc[j][2 * h]);
+                    acc[j][2 * h + 1] = fmaf(w[h], x.y, acc[j][2 * h + 1]);
+                  }
+              }
+              __syncwarp();
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              uint32_t bfr[4];
+              ldsm4_t(va + tile_off(kb + (mat & 1) * 8 + r8, 2 * j + (mat >> 1)),
+                      bfr);
               mma16816(acc[2 * j], pf, bfr[0], bfr[1], E());
               mma16816(acc[2 * j + 1], pf, bfr[2], bfr[3], E());
+            }
           }
         }
         __syncwarp();
@@ -545,8 +536,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           l += __shfl_xor_sync(0xffffffffu, l, 1);
           l += __shfl_xor_sync(0xffffffffu, l, 2);
           if (t4 == 0) {
-            s_m[warp * ROWS + h * 8 + g8] = mx[h];
-            s_l[warp][h * 8 + g8] = l;
+            c.m[warp][h * 8 + g8] = mx[h];
+            c.l[warp][h * 8 + g8] = l;
           }
         }
       named_bar(1, kConsumers * 32);
@@ -556,11 +547,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           float top = kNegInf;
 #pragma unroll
           for (int w = 0; w < kConsumers; ++w)
-            top = fmaxf(top, s_m[w * ROWS + r]);
+            top = fmaxf(top, c.m[w][r]);
           float l = 0.f;
 #pragma unroll
           for (int w = 0; w < kConsumers; ++w)
-            l += s_l[w][r] * factor(s_m[w * ROWS + r], top);
+            l += c.l[w][r] * factor(c.m[w][r], top);
           const float f = factor(mx[h], top);
 #pragma unroll
           for (int j = 0; j < D / 8; ++j) {
@@ -568,8 +559,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             acc[j][2 * h + 1] *= f;
           }
           if (warp == 0 && t4 == 0) {
-            s_M[r] = top;
-            s_L[r] = l;
+            c.M[r] = top;
+            c.L[r] = l;
           }
         }
       // turns: 3 -> 2, 1 -> (after) 0, 2 -> 0 through one buffer, in a fixed
@@ -600,19 +591,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       if (warp == 0) {
         float4* const mine = reinterpret_cast<float4*>(red);
         // rows that are not finite and do not see all that was multiplied
-        const int key0 = (walk.s.tile0 + g.t0) * TK;
-        const int key1 = min((walk.s.tile0 + g.t1) * TK, walk.s.kv);
-        uint32_t bad[2];
+        if (!CAREFUL) {
+          const int key0 = (walk.s.tile0 + g.t0) * TK;
+          const int key1 = min((walk.s.tile0 + g.t1) * TK, walk.s.kv);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = h * 8 + g8;
-          float z = 0.f;
+          for (int h = 0; h < 2; ++h) {
+            const int r = h * 8 + g8;
+            float z = 0.f;
 #pragma unroll
-          for (int j = 0; j < D / 8; ++j)
-            z = fmaf(acc[j][2 * h + 1], 0.f, fmaf(acc[j][2 * h], 0.f, z));
-          bad[h] = __ballot_sync(0xffffffffu,
-                                 r < nrows && s_L[r] != 0.f && !(z == 0.f) &&
-                                     (hi[h] < key1 || lo[h] > max(key0, any_lo)));
+            for (int j = 0; j < D / 8; ++j)
+              z = fmaf(acc[j][2 * h + 1], 0.f, fmaf(acc[j][2 * h], 0.f, z));
+            if (r < nrows && c.L[r] != 0.f && !(z == 0.f) &&
+                (hi[h] < key1 || lo[h] > max(key0, any_lo)))
+              c.redo = 1;
+          }
         }
         const int slot = 2 * blockIdx.x + (g.starts ? 1 : 0);
         if (SPLIT && p.split > 1) {  // joined over the cluster below
@@ -625,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         for (int h = 0; h < 2; ++h) {
           const int r = h * 8 + g8;
           if (r >= nrows || (SPLIT && p.split > 1)) continue;
-          const float top = s_M[r], l = s_L[r];
+          const float top = c.M[r], l = c.L[r];
           if (whole) {
             const int row = g.block * ROWS + r;
             const long long tok = walk.s.q0 + (long long)(row / p.group);
@@ -652,40 +644,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                   make_float2(top, l);
           }
         }
-        if (bad[0] | bad[1]) {
-          // once more over their own keys, 32 columns a lane
-          __syncwarp();
-          constexpr int PARTS = D / 32;
-          for (int task = lane; task < ROWS * PARTS; task += 32) {
-            const int r = task / PARTS, col = task % PARTS * 32;
-            if (!((r < 8 ? bad[0] : bad[1]) >> (r % 8 * 4) & 15u)) continue;
-            const int row = g.block * ROWS + r, tok = row / p.group;
-            const int head = g.head * p.group + row % p.group;
-            const int x = walk.s.kv - walk.s.len + tok;
-            const long long at = walk.s.q0 + (long long)tok;
-            float y[32];
-            exact_columns<E, D>(
-                p, g.n, g.head,
-                static_cast<const E*>(p.q) + at * p.q_row + (long long)head * D,
-                max(key0, p.window > 0 ? x - p.window + 1 : 0),
-                min(key1, p.causal ? x + 1 : key1), s_M[r], col, y);
-            const float inv = 1.f / s_L[r];
-            E* o = static_cast<E*>(p.out) + (at * p.hq + head) * D + col;
-            float* part = p.part_o + ((long long)slot * ROWS + r) * D + col;
-            for (int e = 0; e < 32; e += 2)
-              if (SPLIT && p.split > 1)
-                reinterpret_cast<float2*>(
-                    &mine[(col + e) / 8 * 32 + r % 8 * 4 + e % 8 / 2])[r / 8] =
-                    make_float2(y[e], y[e + 1]);
-              else if (whole)
-                *reinterpret_cast<uint32_t*>(o + e) =
-                    pack2<E>(y[e] * inv, y[e + 1] * inv);
-              else
-                *reinterpret_cast<float2*>(part + e) = make_float2(y[e], y[e + 1]);
-          }
-        }
         if (!SPLIT && g.starts && !g.ends && lane == 0) {
-          const int last = (int)((g.item_end - 1) / per);
+          const int last = (int)((g.item_end - 1) / c.per);
           p.meta[2 * blockIdx.x] = make_int4(g.n, g.head, g.block, last);
           p.meta[2 * blockIdx.x + 1] =
               make_int4(walk.s.q0, walk.s.len, walk.s.kv, 0);
@@ -694,15 +654,120 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       named_bar(1, kConsumers * 32);
     }
   }
+}
+
+// The run once more, with barriers as at the start.
+template <typename E, int D, bool SPLIT>
+__device__ __noinline__ void serve_again(const PagedAttnParams& p,
+                                         const CUtensorMap& tk,
+                                         const CUtensorMap& tv, int box, char* sm,
+                                         Shared& c) {
+  using S = Shape<D>;
+  if (threadIdx.x == 0) {
+    S::init(S::barriers(sm) + 2 * S::kStages);
+    fence_mbar_init();
+  }
   __syncthreads();
+  Walk walk;
+  walk.w = c.per * blockIdx.x;
+  walk.w_end = min(walk.w + c.per, c.total);
+  walk.n = c.n;
+  walk.base = c.base;
+  walk.s = seq_work(p, c.n);
+  Segment g;
+  serve<E, D, SPLIT, true>(p, tk, tv, box, sm, c, walk, g);
+  __syncthreads();
+}
+
+template <typename E, int D, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    paged_rows_kernel(const __grid_constant__ PagedAttnParams p,
+                      const __grid_constant__ CUtensorMap tk,
+                      const __grid_constant__ CUtensorMap tv, int box) {
+  using S = Shape<D>;
+  extern __shared__ char smem_raw[];
+  char* sm = reinterpret_cast<char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  __shared__ Shared c;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  if (tid == 0) {
+    c.abort = c.redo = 0;
+    c.n = p.N;
+    S::init(S::barriers(sm));
+    fence_mbar_init();
+    prefetch_tmap(&tk);
+    prefetch_tmap(&tv);
+  }
+  griddep_wait();  // nothing above touches what earlier kernels write
+
+  // where this CTA's run lies: thread t sums the sequences [t * per, ...)
+  const int per_t = (p.N + kThreads - 1) / kThreads;
+  const int n_lo = min(p.N, tid * per_t), n_hi = min(p.N, n_lo + per_t);
+  long long mine = 0;
+  bool bad = false;
+  for (int n = n_lo; n < n_hi; ++n) {
+    const Seq s = seq_work(p, n);
+    mine += seq_units<SPLIT>(p, s);
+    bad = bad || !s.ordered;
+  }
+  long long scan = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const long long up = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += up;
+  }
+  if (lane == 31) c.sum[warp] = scan;
+  const bool skip = __syncthreads_or(bad);
+  long long total = 0, before = scan - mine;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) before += c.sum[i];
+    total += c.sum[i];
+  }
+  if (skip) total = 0;
+  // (a split call has a block for every part)
+  const long long per =
+      SPLIT ? 1 : (total + gridDim.x - 1) / gridDim.x;
+  Walk walk;
+  walk.w = per * blockIdx.x;
+  walk.w_end = walk.w + per < total ? walk.w + per : total;
+  if (walk.w < walk.w_end && mine > 0 && walk.w >= before &&
+      walk.w < before + mine) {
+    long long base = before;
+    int n = n_lo;
+    for (; n < n_hi; ++n) {
+      const long long u = seq_units<SPLIT>(p, seq_work(p, n));
+      if (walk.w < base + u) break;
+      base += u;
+    }
+    c.n = n;
+    c.base = base;
+    c.total = total;
+    c.per = per;
+  }
+  __syncthreads();
+  walk.n = c.n;
+  walk.base = c.base;
+  if (tid == 0 && !SPLIT) p.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (walk.n >= p.N) return;  // no work for this CTA
+  walk.s = seq_work(p, walk.n);
+
+  Segment g;
+  serve<E, D, SPLIT, false>(p, tk, tv, box, sm, c, walk, g);
+  __syncthreads();
+  if (c.redo && !c.abort)
+    serve_again<E, D, SPLIT>(p, tk, tv, box, sm, c);
   if (SPLIT && p.split > 1) {
     // ---- join the cluster's parts of the item ----------------------------------
     cluster_sync();
-    if (warp < kConsumers) join_cluster<E, D>(p, walk.s, g, red, s_M, s_L);
+    if (warp < kConsumers)
+      join_cluster<E, D>(
+          p, walk.s, g,
+          reinterpret_cast<float*>(sm + S::kStages * 2 * S::kTile), c.M, c.L);
     __syncwarp();
     cluster_sync();  // (the others may still read this one's)
   }
-  if (tid == 0 && *abort_flag) {
+  if (tid == 0 && c.abort) {
     record_status(p.status, GDN_ERR_TIMEOUT);
     wait_out_copies();
   }

@@ -41,7 +41,8 @@
 // see), so ragged batches, few long items and many short ones fill the machine
 // alike. A run that holds a whole item writes its output; pieces of a cut item
 // go to the workspace in fp32 and paged_merge.cu joins them in the order
-// of the runs.
+// of the runs. A run that may have spoilt a result (see paged.cuh on hidden
+// values) is handed out a second time.
 //
 // Warps: 0-3 and 4-7 the softmax and epilogue of row tiles 0 and 1 (their TMEM
 // lanes), 8 looks pages up and issues TMA copies into a ring of key and value
@@ -83,7 +84,7 @@ struct Shape {
   static constexpr int kSmem = 1024 + 2 * kQ + kRing * kTile + kStage + kMisc;
 };
 static_assert(Shape<128>::kSmem <= 227 * 1024, "shared memory");
-static_assert(Shape<64>::kRing * 16 + 176 <= 512, "barriers");
+static_assert(Shape<64>::kRing * 16 + 192 <= 512, "barriers");
 
 // ---- the work list -----------------------------------------------------------
 struct Slot {
@@ -237,6 +238,7 @@ struct Segment {
   int first[2], last[2];  // each row tile's share of them
   int starts, ends;       // holds the item's first / last tile
   int last_run;           // the run that holds the item's last tile
+  int careful;            // a second time
 };
 
 __device__ __forceinline__ bool next_segment(const PagedAttnParams& p, int tt,
@@ -382,6 +384,194 @@ __host__ __device__ constexpr uint32_t idesc_of<__half>(int N, bool b_mn) {
   return idesc_bf16(128, N, false, b_mn) & ~((1u << 7) | (1u << 10));
 }
 
+// For tiles that hold a value which is not finite and hidden from some row: O +
+// P V of one key tile and a row a lane, key by key, over the keys [lo, hi) that
+// the row sees, with the weights that lie in TMEM at t_p for the product. The
+// tensor core makes its product all the same and spoils O, so the row is kept in
+// `out` and put back when that is done. (Some 60 us a tile.)
+template <typename E, int D>
+__device__ __noinline__ void add_by_key(uint32_t t_p, uint32_t t_o, const char* v,
+                                        int lo, int hi, bool fresh, float* out) {
+#pragma unroll 1
+  for (int col = 0; col < D; col += 16) {
+    float o[16];
+    tmem_ld16(t_o + col, o);
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = fresh ? 0.f : o[e];
+    const char* const half = v + (col / 64) * (TK * 128);
+#pragma unroll 1
+    for (int k0 = 0; k0 < TK; k0 += 32) {
+      float p[16];  // pairs of weights
+      tmem_ld16(t_p + k0 / 2, p);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const int key = k0 + i;
+        const float2 w2 = unpack2(__float_as_uint(p[i / 2]), E());
+        const float w = i & 1 ? w2.y : w2.x;
+        const bool sees = key >= lo && key < hi;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint4 x = *reinterpret_cast<const uint4*>(
+              half + sw128(key, (col % 64) / 8 + c));
+          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 y = unpack2(u[e], E());
+            float* const a = o + c * 8 + 2 * e;
+            a[0] = sees ? fmaf(w, y.x, a[0]) : a[0];
+            a[1] = sees ? fmaf(w, y.y, a[1]) : a[1];
+          }
+        }
+      }
+      __syncwarp();
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) out[col + e] = o[e];
+  }
+}
+
+// A kept row back to O.
+template <int D>
+__device__ __noinline__ void put_row(uint32_t t_o, const float* row) {
+#pragma unroll 1
+  for (int col = 0; col < D; col += 16) {
+    uint32_t u[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(row[col + e]);
+    tmem_st16(t_o + col, u);
+  }
+  tmem_st_wait();
+}
+
+// The softmax of a segment's key tiles the second time, for row tile t (a row a
+// thread): as in the kernel (to the order of its additions), but plainly, and
+// with a look through the values of tiles that some row sees in part. (`at`
+// counts the row tile's steps so far, `outs` its outputs, `probes` the steps made
+// here; pos: key tiles before the segment.)
+struct RowSums {
+  float ref, sum;
+  bool ok;
+};
+template <typename E, int D>
+__device__ __noinline__ RowSums careful_keys(const PagedAttnParams& p,
+                                             const Segment& g, char* kv,
+                                             uint64_t* bars, uint64_t* kv_full,
+                                             volatile uint32_t* by_key,
+                                             volatile int* abort_flag, int t,
+                                             uint32_t t_s, uint32_t t_o, int pos,
+                                             uint32_t at, uint32_t outs,
+                                             uint32_t probes) {
+  using S = Shape<D>;
+  uint64_t *s_full = bars + 4 + t, *p_full = bars + 6 + 2 * t,
+           *o_full = bars + 10 + t, *probed = bars + 22 + t;
+  const int r = threadIdx.x & 127, lane = threadIdx.x % 32;
+  const int tt = 128 / p.group;
+  const int x = g.before + g.tok + t * tt + r / p.group;
+  const int hi = p.causal ? min(x + 1, g.kv) : g.kv;
+  const int lo = p.window > 0 ? max(0, x - p.window + 1) : 0;
+  const bool valid = r < g.ntok[t] * p.group;
+  // keys [free_lo, free_hi) are seen by every row of the tile
+  const int x0 = g.before + g.tok + t * tt;
+  const int free_hi = p.causal ? min(x0 + 1, g.kv) : g.kv;
+  const int free_lo = p.window > 0 ? x0 + g.ntok[t] - p.window : 0;
+  const int first = g.first[t], last = g.last[t];
+  RowSums y{kNegInf, 0.f, false};
+#pragma unroll 1
+  for (int j = first; j < last; ++j) {
+    if (!warp_wait(s_full, at & 1, abort_flag)) return y;
+    tc_fence_after();
+    ++at;
+    const uint32_t v = 2u * (uint32_t)(pos + j - g.s0) + 1u, slot = v % S::kRing;
+    if (!warp_wait(&kv_full[slot], (v / S::kRing) & 1, abort_flag)) return y;
+    char* const values = kv + slot * S::kTile;
+    const int key0 = j * TK, key = key0 + r;
+    uint32_t z = 0;
+#pragma unroll 1
+    for (int i = 0; i < S::kHalves * 8; ++i) {  // (lanes in different banks)
+      uint4* const x16 = reinterpret_cast<uint4*>(
+          values + (i / 8) * (TK * 128) + r * 128 + (i + lane) % 8 * 16);
+      if (key >= g.hi || key < g.lo)
+        *x16 = make_uint4(0u, 0u, 0u, 0u);  // seen by no row
+      else if (key0 < free_lo || key0 + TK > free_hi)
+        z = probe8<E>(*x16, z);
+    }
+    fence_proxy_async();
+    if (probe_hit(z)) by_key[t] = at;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(probed);
+    if (!warp_wait(probed, probes++ & 1, abort_flag)) return y;
+    const bool spoilt = by_key[t] == at;
+    float top = kNegInf;
+#pragma unroll 1
+    for (int i = 0; i < TK; i += 32) {
+      float s[32];
+      tmem_ld32(t_s + i, s);
+      tmem_ld_wait();
+      mask32(s, lo - key0, hi - key0, i);
+      top = fmaxf(top, max32(s));
+    }
+    top *= p.scale_log2;
+    if (__any_sync(0xffffffffu, valid && top > y.ref + kSlack)) {
+      const float now = fmaxf(y.ref, top);
+      const float f = factor(y.ref, now);
+      y.ref = now;
+      y.sum *= f;
+#pragma unroll 1
+      for (int i = 0; j > first && i < D; i += 16) {
+        float o[16];
+        tmem_ld16(t_o + i, o);
+        tmem_ld_wait();
+        uint32_t u[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * f);
+        tmem_st16(t_o + i, u);
+      }
+    }
+    const float m = y.ref == kNegInf ? 0.f : y.ref;
+    uint64_t part[2] = {0, 0};  // (the kernel's order of additions)
+#pragma unroll 1
+    for (int i = 0; i < TK; i += 32) {  // (weights over scores read already)
+      float s[32];
+      tmem_ld32(t_s + i, s);
+      tmem_ld_wait();
+      mask32(s, lo - key0, hi - key0, i);
+      uint32_t u[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float a = ex2(fmaf(s[2 * e], p.scale_log2, -m));
+        const float b = ex2(fmaf(s[2 * e + 1], p.scale_log2, -m));
+        part[e & 1] = add2(part[e & 1], pair(a, b));
+        u[e] = pack2<E>(a, b);
+      }
+      tmem_st16(t_s + i / 2, u);
+    }
+    float even, odd;
+    unpair(add2(part[0], part[1]), even, odd);
+    y.sum += even + odd;
+    tmem_st_wait();
+    float o[D];
+    if (spoilt)
+      add_by_key<E, D>(t_s, t_o, values, lo - key0, hi - key0, j == first, o);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(p_full);
+      mbar_arrive(p_full + 1);
+    }
+    if (spoilt) {
+      if (!(j + 1 < last ? warp_wait(s_full, at & 1, abort_flag)
+                         : warp_wait(o_full, outs & 1, abort_flag)))
+        return y;
+      tc_fence_after();
+      put_row<D>(t_o, o);
+    }
+  }
+  y.ok = true;
+  return y;
+}
+
 template <typename E, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tiles_kernel(const __grid_constant__ PagedAttnParams p,
@@ -405,7 +595,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* o_free = bars + 12;   // [2]
   uint64_t* seg_full = bars + 14;   // [kSegs]
   uint64_t* seg_empty = bars + 18;  // [kSegs]
-  uint64_t* kv_full = bars + 22;
+  uint64_t* probed = bars + 22;     // [2]
+  uint64_t* kv_full = bars + 24;
   uint64_t* kv_empty = kv_full + S::kRing;
   long long* s_sum = reinterpret_cast<long long*>(misc + 512);  // [12]
   long long* s_base = s_sum + 12;
@@ -413,8 +604,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(misc + 640);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 644);
   int* s_n = reinterpret_cast<int*>(misc + 648);
-  Segment* s_seg = reinterpret_cast<Segment*>(misc + 656);  // [kSegs]
-  static_assert(656 + kSegs * sizeof(Segment) <= S::kMisc, "segments");
+  // a result may hold what its row does not see
+  volatile int* redo = reinterpret_cast<volatile int*>(misc + 652);
+  // [2]: the row tile's last step that its softmax warps made key by key
+  volatile uint32_t* by_key = reinterpret_cast<volatile uint32_t*>(misc + 656);
+  // [8]: the softmax warp is at the first half of a step
+  volatile uint32_t* busy = reinterpret_cast<volatile uint32_t*>(misc + 664);
+  Segment* s_seg = reinterpret_cast<Segment*>(misc + 696);  // [kSegs]
+  static_assert(696 + kSegs * sizeof(Segment) <= S::kMisc, "segments");
 
   const int tid = threadIdx.x, lane = tid % 32;
   const int warp = uniform(tid / 32);
@@ -427,9 +624,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t count = 1;
     if (bar >= kv_empty)
       count = 2;
-    else if ((bar >= p_full && bar < o_full) || bar == o_free || bar == o_free + 1)
+    else if ((bar >= p_full && bar < o_full) || (bar >= o_free && bar < seg_full) ||
+             (bar >= probed && bar < kv_full))
       count = 4;
-    else if (bar >= seg_empty && bar < kv_full)
+    else if (bar >= seg_empty && bar < probed)
       count = kSegReaders;
     mbar_init(bar, count);
     fence_mbar_init();
@@ -437,6 +635,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     *abort_flag = 0;
     *s_n = -1;
+    *redo = 0;
+    by_key[0] = by_key[1] = 0;
+    for (int i = 0; i < 8; ++i) busy[i] = 0;
     prefetch_tmap(&tq);
     prefetch_tmap(&tk);
     prefetch_tmap(&tv);
@@ -534,42 +735,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (work && warp == 9) {
       // ---- scheduler: hands the run's segments out, loads their queries ----------
       if (lane == 0) {
-        Walk walk;
-        walk.slots = slots;
-        walk.w = w0;
-        walk.w_end = w1;
-        walk.base = *s_base;
-        walk.at = *s_place;
-        walk.s = slot_at(p, walk.at, tt);
         uint32_t loads[2] = {0, 0};
-        bool more = true;
-        for (int i = 0; more; ++i) {
-          if (i >= kSegs &&
-              !fast_wait(&seg_empty[i % kSegs], (i / kSegs - 1) & 1, abort_flag))
-            break;
-          Segment g;
-          more = next_segment(p, tt, per, walk, g);
-          if (!more) g.n = -1;
-          s_seg[i % kSegs] = g;
-          mbar_arrive(&seg_full[i % kSegs]);
-          if (!more || g.s0 == g.s1) continue;
-          // its queries, a row tile's once the last scores of that row tile
-          // are done with theirs
-          bool ok = true;
+        int i = 0;  // segments handed out
+        bool ok = true;
+        // a second time if a result of the first may hold hidden values
+        for (int pass = 0; pass < 2; ++pass) {
+          Walk walk;
+          walk.slots = slots;
+          walk.w = w0;
+          walk.w_end = w1;
+          walk.base = *s_base;
+          walk.at = *s_place;
+          walk.s = slot_at(p, walk.at, tt);
+          for (; ok; ++i) {
+            if (i >= kSegs)
+              ok = fast_wait(&seg_empty[i % kSegs], (i / kSegs - 1) & 1,
+                             abort_flag);
+            Segment g;
+            if (!ok || !next_segment(p, tt, per, walk, g)) break;
+            g.careful = pass;
+            s_seg[i % kSegs] = g;
+            mbar_arrive(&seg_full[i % kSegs]);
+            if (g.s0 == g.s1) continue;
+            // its queries, a row tile's once the last scores of that row tile
+            // are done with theirs
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (!ok || g.first[t] >= g.last[t]) continue;
-            if (loads[t] > 0)
-              ok = fast_wait(&q_empty[t], (loads[t] - 1) & 1, abort_flag);
-            if (!ok) continue;
-            ++loads[t];
-            mbar_arrive_expect_tx(&q_full[t], S::kHalves * tt * p.group * 128);
+            for (int t = 0; t < 2; ++t) {
+              if (!ok || g.first[t] >= g.last[t]) continue;
+              if (loads[t] > 0)
+                ok = fast_wait(&q_empty[t], (loads[t] - 1) & 1, abort_flag);
+              if (!ok) continue;
+              ++loads[t];
+              mbar_arrive_expect_tx(&q_full[t], S::kHalves * tt * p.group * 128);
 #pragma unroll
-            for (int h = 0; h < S::kHalves; ++h)
-              tma_load_4d(sm_q + t * S::kQ + h * (TM * 128), &tq, &q_full[t],
-                          h * 64, g.head * p.group, g.q0 + g.tok + t * tt, 0);
+              for (int h = 0; h < S::kHalves; ++h)
+                tma_load_4d(sm_q + t * S::kQ + h * (TM * 128), &tq, &q_full[t],
+                            h * 64, g.head * p.group, g.q0 + g.tok + t * tt, 0);
+            }
           }
-          if (!ok) break;
+          if (!ok || i == 0 ||
+              !fast_wait(&seg_empty[(i - 1) % kSegs], ((i - 1) / kSegs) & 1,
+                         abort_flag) ||
+              !*redo)
+            break;
+        }
+        if (ok) {
+          s_seg[i % kSegs].n = -1;
+          mbar_arrive(&seg_full[i % kSegs]);
         }
       }
       __syncwarp();
@@ -732,6 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float c = p.scale_log2;
       int pos = 0;  // key tiles (of any item) before this segment's
       int steps = 0, outs = 0;  // of this row tile, over all segments
+      int probes = 0;
       bool ok = true;
       const int rt = r / p.group, rh = r - rt * p.group;
       for (int i_seg = 0; ok; ++i_seg) {
@@ -750,7 +963,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int any_lo = g.lo, any_hi = g.hi;
         const int s0 = g.s0, first = g.first[t], last = g.last[t];
         float ref = kNegInf, sum = 0.f;
-        for (int j = first; j < last; ++j) {
+        int begin = first;
+        if (g.careful) {
+          const RowSums y = careful_keys<E, D>(p, g, sm_kv, bars, kv_full, by_key,
+                                               abort_flag, t, t_s, t_o, pos, steps,
+                                               outs, probes);
+          ok = y.ok;
+          if (!ok) break;
+          ref = y.ref;
+          sum = y.sum;
+          steps += last - first;
+          probes += last - first;
+          begin = last;
+        }
+        for (int j = begin; j < last; ++j) {
           ok = warp_wait(&s_full[t], steps & 1, abort_flag);
           if (!ok) break;
           tc_fence_after();
@@ -763,6 +989,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int see_lo = lo - key0, see_hi = hi - key0;
           tmem_ld32(t_s, x[0]);
           tmem_ld32(t_s + 32, x[1]);
+          // Let the other row tile's warp of this scheduler finish its first
+          // half (some 40 cycles a look, and then on in any case: it may have no
+          // such step). The row tiles fall into step with each other otherwise:
+          // their exponentials share the scheduler, then the tensor core waits
+          // (2048 tokens over 65536 keys 725 us, 880 without the looks; before
+          // masked tiles they cost more than they give).
+#pragma unroll 1
+          for (int i = 0; !masked && i < 8 && busy[warp ^ 4] != 0; ++i) {
+          }
+          __syncwarp();
+          if (lane == 0) busy[warp] = 1;
           tmem_ld_wait();
           tmem_ld32(t_s + 64, x[2]);
           tmem_ld32(t_s + 96, x[3]);
@@ -835,7 +1072,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st_wait();
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&p_full[2 * t]);
+              if (lane == 0) {
+                mbar_arrive(&p_full[2 * t]);
+                busy[warp] = 0;
+              }
             }
           }
           float pa, pb;
@@ -884,7 +1124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool none = !some || (whole && hi <= lo);  // sees nothing: 0
         const float scale = 1.f / sum;
         const int chunks = whole ? D / 64 : D / 32;
-        uint32_t odd = 0;  // 32 columns of the row each: not all are finite
+        uint32_t odd = 0;  // a column of the row is not finite
 #pragma unroll 1
         for (int i = 0; i < chunks; ++i) {
           uint32_t u[32];
@@ -896,7 +1136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               float o[32];
               tmem_ld32(t_o + i * 64 + h * 32, o);
               tmem_ld_wait();
-              odd |= nonfinite(o) << (2 * i + h);
+              odd |= nonfinite(o);
 #pragma unroll
               for (int e = 0; e < 16; ++e)
                 u[h * 16 + e] = pack2<E>(o[2 * e] * scale, o[2 * e + 1] * scale);
@@ -905,7 +1145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float o[32];
             tmem_ld32(t_o + i * 32, o);
             tmem_ld_wait();
-            odd |= nonfinite(o) << i;
+            odd |= nonfinite(o);
 #pragma unroll
             for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e]);
           }
@@ -938,34 +1178,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         (lane & 7) * 16) = y[e];
           __syncwarp();
         }
-        // a row that is not finite and does not see all that was multiplied,
-        // once more over its own keys
+        // a row that is not finite and does not see all that was multiplied
         const int low = max(lo, first * TK), high = min(hi, last * TK);
         const bool bad = valid && !none && odd != 0 &&
                          (low > max(any_lo, first * TK) ||
                           high < min(any_hi, last * TK));
-        if (__any_sync(0xffffffffu, bad)) {
-          if (bad) {
-            for (int col = 0; col < D; col += 32) {
-              if (!(odd >> (col / 32) & 1u)) continue;
-              float y[32];
-              exact_columns<E, D>(p, g.n, g.head,
-                                  static_cast<const E*>(p.q) + tok * p.q_row +
-                                      (long long)head * D,
-                                  low, high, ref, col, y);
-              char* to = dst + row_off + col * (whole ? 2 : 4);
-              for (int e = 0; e < 32; e += 2) {
-                if (whole)
-                  *reinterpret_cast<uint32_t*>(to + e * 2) =
-                      pack2<E>(y[e] * scale, y[e + 1] * scale);
-                else
-                  *reinterpret_cast<float2*>(to + e * 4) =
-                      make_float2(y[e], y[e + 1]);
-              }
-            }
-          }
-          __syncwarp();
-        }
+        if (bad) *redo = 1;
         if (tid == 0 && g.starts && !g.ends) {
           p.meta[2 * blockIdx.x] =
               make_int4(g.n, g.head, g.block, g.last_run);

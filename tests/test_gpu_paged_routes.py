@@ -8,7 +8,8 @@ import pytest
 import torch
 
 from oracle import paged
-from test_gpu_paged import attend, close, gpu, make, paths, table_of, widen
+from test_gpu_paged import (attend, close, gpu, hidden_values, make, paths,
+                            table_of, widen)
 
 pytestmark = pytest.mark.gpu
 
@@ -114,3 +115,76 @@ def test_append_offsets_that_start_late(lib, cuda_device):
     for x, r in ((out[:, 4:13], ref[0]), (kc, ref[1]), (vc, ref[2])):
         err = np.abs(x.cpu().double().numpy() - r)
         assert (err <= 2.0 ** -8 * np.abs(r) + 2.0 ** -19).all()
+
+
+# ---- hidden values ------------------------------------------------------------
+@pytest.mark.parametrize("bad", [float("nan"), -float("inf")])
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (64, "f16"), (128, "f16")])
+@pytest.mark.parametrize("new,keys,window", [((3,), (200,), 0), ((3,), (200,), 40),
+                                             ((150,), (150,), 0),
+                                             ((150,), (400,), 60)])
+def test_hidden_values_of_both_types(lib, cuda_device, d, dtype, bad, new, keys,
+                                     window):
+    s = make(45, hq=6, hkv=2, d=d, dtype=dtype, new=new, keys=keys, poison=False)
+    for t in tables(s):
+        hidden_values(lib, cuda_device, t, bad, new, keys, window)
+
+
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "f16")])
+@pytest.mark.parametrize("new,window", [(40, 0), (40, 30000), (3, 0), (3, 30000)])
+def test_hidden_values_in_long_caches(lib, cuda_device, new, window, d, dtype):
+    """What a hidden value costs does not grow with the cache: 320 sequences on
+    the same 70000 keys, so that a block has whole items. (Key by key over the
+    whole cache, a thread's dependent loads of 0.3 us alone would take 20 ms an
+    item and group of 32 columns; the calls take some 3 ms.)"""
+    dev, N, L = cuda_device, 320, 70000
+    s = make(46, hq=4, hkv=1, d=d, dtype=dtype, page=256, new=(new,), keys=(L,),
+             poison=False)
+    x0, page = L - new, 256
+
+    def put(key, col, value):
+        at = int(s["page_table"][0, key // page]), 0, key % page
+        s["v_cache"][at + (col,)] = value
+
+    t = np.arange(new)
+    inf_at, nan_at = x0 + new // 4, x0 + new // 2
+    edge = x0 - window + 1 + new // 3  # seen by the tokens up to new // 3
+    clean = dict(s, v_cache=s["v_cache"].clone())
+    put(inf_at, 7, float("inf"))
+    put(nan_at, slice(None), float("nan"))
+    sees_inf, sees_nan = x0 + t >= inf_at, x0 + t >= nan_at
+    if window:
+        put(edge, slice(None), float("nan"))
+        sees_nan |= t <= new // 3
+    put7 = int(s["page_table"][0, inf_at // page]), 0, inf_at % page, 7
+    clean["v_cache"][put7] = 0.0
+    ref, rl, mag = (x[0] for x in paged.attend(
+        clean["q"], clean["k_cache"], clean["v_cache"], s["page_table"],
+        s["kv_lens"], window=window))
+    u = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -11
+    bound = u * (np.abs(ref) + 1.02 * mag) + 4e-4 * mag
+    if dtype == "f16":
+        bound = bound + L * 2.0 ** -25 * float(clean["v_cache"].abs().max())
+    args = [s["q"].to(dev).expand(N, -1, -1, -1).contiguous(),
+            s["k_cache"].to(dev), s["v_cache"].to(dev),
+            s["page_table"].to(dev).expand(N, -1).contiguous(),
+            s["kv_lens"].to(dev).expand(N).contiguous()]
+    for path in ([lib.GDN_PAGED_ROWS, lib.GDN_PAGED_TILES] if new < 10
+                 else [lib.GDN_PAGED_TILES]):
+        at = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        for _ in range(2):
+            at[0].record()
+            o, lse = lib.gdn_paged_attn(*args, window=window, path=path,
+                                        return_lse=True)
+            at[1].record()
+        torch.cuda.synchronize()
+        assert lib.gdn_device_status() == 0
+        assert at[0].elapsed_time(at[1]) < 30.0
+        o, lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
+        assert (np.abs(lse - rl) <= 2e-4 + 1e-6 * np.abs(rl)).all()
+        assert np.isnan(o[:, sees_nan]).all()
+        some = ~sees_nan & sees_inf
+        assert np.isposinf(o[:, some, :, 7]).all()
+        o[..., 7][:, some] = ref[some, :, 7]
+        rest = ~sees_nan
+        assert (np.abs(o - ref)[:, rest] <= bound[rest]).all()
