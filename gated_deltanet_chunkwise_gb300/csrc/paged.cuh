@@ -144,6 +144,18 @@ constexpr float kNegInf = -INFINITY;
 // the same relative rounding as 16-bit factors, and the accumulators are
 // rarely rescaled.
 constexpr float kSlack = 8.f;
+// The reference stands this far (in powers of two) below the maximum that it
+// was taken from. bf16 weights have fp32's range; fp16's normal ones end at
+// 2^-14 and their last at 2^-25, so a weight of 1 for the largest score would
+// round the many small ones of a long cache behind one dominant key away or up
+// (an attention sink, the others 17 below it in natural logarithms, 100000 keys:
+// their part of the output is off by a quarter), while the sum takes them as they
+// are. With 2^7 for the largest score weights stay below 2^15, inside the type,
+// and reach down to 2^-32 of it.
+template <typename E>
+constexpr float kLift = 0.f;
+template <>
+constexpr float kLift<__half> = 7.f;
 // What weights relative to `was` are multiplied by to be relative to `now`.
 // With no score above -inf yet the reference is 0: the sums are 0 then, or
 // NaN if a score was NaN, which stays one.

@@ -444,7 +444,7 @@ __device__ __forceinline__ void serve(const PagedAttnParams& p,
                   if (key >= hi[e >> 1] || key < lo[e >> 1]) x = kNegInf;
                 }
                 s[j][e] = x;
-                grow = grow || !(x <= mx[e >> 1] + kSlack);  // (NaN too)
+                grow = grow || !(x <= mx[e >> 1] + kSlack + kLift<E>);  // (NaN too)
               }
           if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -453,7 +453,7 @@ __device__ __forceinline__ void serve(const PagedAttnParams& p,
                                   fmaxf(s[1][2 * h], s[1][2 * h + 1]));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float now = fmaxf(mx[h], top);
+                const float now = fmaxf(mx[h], top - kLift<E>);
                 const float f = factor(mx[h], now);
                 mx[h] = now;
                 sum[h] *= f;

@@ -21,8 +21,9 @@
 // for the case below.) The first half of P goes to work while the second is
 // computed (722 -> 671 us).
 //
-// The reference m follows the running maximum only when a score passes it by
-// more than 2^8 (weights stay below 2^8; sums and O are fp32), so O, which
+// The reference m (for fp16 2^7 below the maximum) follows the running maximum
+// only when a score passes it by more than 2^8 (weights stay below 2^8, fp16
+// ones below 2^15; sums and O are fp32), so O, which
 // lives in TMEM, is rarely rescaled, and the softmax warps do it themselves:
 // S(j + 1)'s barrier already says that O += P(j) V(j) is complete. Weights are
 // rounded to 16 bits for their product (2^-9 on the average, as the output
@@ -513,8 +514,8 @@ __device__ __noinline__ RowSums careful_keys(const PagedAttnParams& p,
       top = fmaxf(top, max32(s));
     }
     top *= p.scale_log2;
-    if (__any_sync(0xffffffffu, valid && top > y.ref + kSlack)) {
-      const float now = fmaxf(y.ref, top);
+    if (__any_sync(0xffffffffu, valid && top > y.ref + kSlack + kLift<E>)) {
+      const float now = fmaxf(y.ref, top - kLift<E>);
       const float f = factor(y.ref, now);
       y.ref = now;
       y.sum *= f;
@@ -1032,9 +1033,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_proxy_async();
           }
-          const bool grow = valid && top > ref + kSlack;
+          const bool grow = valid && top > ref + kSlack + kLift<E>;
           if (__any_sync(0xffffffffu, grow)) {
-            const float now = fmaxf(ref, top);
+            const float now = fmaxf(ref, top - kLift<E>);
             const float f = factor(ref, now);
             ref = now;
             sum *= f;

@@ -515,7 +515,8 @@ int gdn_paged_append(const void* q, int64_t q_stride, const void* k,
  * or not, and an infinity or a NaN among a sequence's own keys and values
  * reaches the tokens that see it and no others. Scores, maxima, sums and
  * accumulators are fp32; weights are rounded to the 16-bit type for their
- * product with V, and the output once. A sequence whose keys do not fit the
+ * product with V (fp16: to 11 bits down to 2^-21 of a row's largest one, to
+ * multiples of 2^-31 of it below), and the output once. A sequence whose keys do not fit the
  * table is skipped (its rows are not written), offsets that decrease or leave
  * [0, T] leave every row unwritten, and a page outside the pool reads as zeros;
  * all three record GDN_ERR_INVALID_ARG. Results do not depend on timing.

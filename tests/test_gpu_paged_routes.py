@@ -188,3 +188,40 @@ def test_hidden_values_in_long_caches(lib, cuda_device, new, window, d, dtype):
         o[..., 7][:, some] = ref[some, :, 7]
         rest = ~sees_nan
         assert (np.abs(o - ref)[:, rest] <= bound[rest]).all()
+
+
+# ---- fp16 weights ---------------------------------------------------------------
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("below", [17.0, 18.0])
+def test_small_f16_weights_behind_a_dominant_key(lib, cuda_device, d, below):
+    """One key whose score stands far above the others': their many small
+    weights count. 304 sequences on the same keys, so that a block has whole
+    items and every weight one reference.
+
+    Bound: weights are rounded relative to 2^7 for the largest score, so each is
+    off by at most 2^-25 2^-7 of it (or 2^-11 of itself): keys 2^-32 and 2^-11
+    of out in all; one rounding of the output (2^-11); scores here are exact to
+    2^-20 (a product of two numbers, all others 0)."""
+    dev, N, L = cuda_device, 304, 100000
+    s = make(47, hq=1, hkv=1, d=d, dtype="f16", page=256, new=(20,), keys=(L,),
+             poison=False)
+    k = torch.zeros_like(s["k_cache"])
+    v = torch.ones_like(s["v_cache"])
+    first = int(s["page_table"][0, 0])
+    k[first, 0, 3, 0] = below
+    v[first, 0, 3] = 0.0
+    q = torch.zeros_like(s["q"])
+    q[..., 0] = 1.0
+    args = [q.to(dev).expand(N, -1, -1, -1).contiguous(), k.to(dev), v.to(dev),
+            s["page_table"].to(dev).expand(N, -1).contiguous(),
+            s["kv_lens"].to(dev).expand(N).contiguous()]
+    for causal in (True, False):
+        seen = (np.arange(L - 20, L) + 1 if causal else np.full(20, L)) - 1.0
+        small = seen * np.exp(-below)
+        ref = (small / (1.0 + small))[None, :, None, None]
+        bound = L * 2.0 ** -32 + ref * (2 * 2.0 ** -11 + 2.0 ** -19)
+        for path in (lib.GDN_PAGED_ROWS, lib.GDN_PAGED_TILES):
+            o = lib.gdn_paged_attn(*args, scale=1.0, causal=causal, path=path)
+            assert lib.gdn_device_status() == 0
+            err = np.abs(o.double().cpu().numpy() - ref)
+            assert (err <= bound).all(), float((err / ref).max())
