@@ -156,6 +156,11 @@ template <typename E>
 constexpr float kLift = 0.f;
 template <>
 constexpr float kLift<__half> = 7.f;
+// From here on a score's product with the scale is rounded before the reference
+// is taken off it, as the reference was: the two differ by up to half a unit of
+// the last place otherwise, which 2^ of turns into infinity where scores pass
+// 2^31 (fp16: 2^25). (In the tile kernel such a run is made a second time.)
+constexpr float kFar = 1048576.f;
 // What weights relative to `was` are multiplied by to be relative to `now`.
 // With no score above -inf yet the reference is 0: the sums are 0 then, or
 // NaN if a score was NaN, which stays one.

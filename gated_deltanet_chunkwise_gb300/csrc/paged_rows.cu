@@ -438,7 +438,7 @@ __device__ __forceinline__ void serve(const PagedAttnParams& p,
             for (int j = 0; j < 2; ++j)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                float x = s[j][e] * p.scale_log2;
+                float x = __fmul_rn(s[j][e], p.scale_log2);  // (see kFar)
                 if (masked) {
                   const int key = key0 + j * 8 + 2 * t4 + (e & 1);
                   if (key >= hi[e >> 1] || key < lo[e >> 1]) x = kNegInf;

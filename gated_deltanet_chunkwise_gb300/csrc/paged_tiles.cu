@@ -447,8 +447,9 @@ __device__ __noinline__ void put_row(uint32_t t_o, const float* row) {
 }
 
 // The softmax of a segment's key tiles the second time, for row tile t (a row a
-// thread): as in the kernel (to the order of its additions), but plainly, and
-// with a look through the values of tiles that some row sees in part. (`at`
+// thread): as in the kernel (to the order of its additions), but plainly, with
+// the care that scores beyond kFar want and a look through the values of tiles
+// that some row sees in part. (`at`
 // counts the row tile's steps so far, `outs` its outputs, `probes` the steps made
 // here; pos: key tiles before the segment.)
 struct RowSums {
@@ -531,6 +532,8 @@ __device__ __noinline__ RowSums careful_keys(const PagedAttnParams& p,
       }
     }
     const float m = y.ref == kNegInf ? 0.f : y.ref;
+    const bool far = __any_sync(0xffffffffu, valid && fabsf(y.ref) >= kFar &&
+                                                 y.ref != kNegInf);
     uint64_t part[2] = {0, 0};  // (the kernel's order of additions)
 #pragma unroll 1
     for (int i = 0; i < TK; i += 32) {  // (weights over scores read already)
@@ -541,8 +544,10 @@ __device__ __noinline__ RowSums careful_keys(const PagedAttnParams& p,
       uint32_t u[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const float a = ex2(fmaf(s[2 * e], p.scale_log2, -m));
-        const float b = ex2(fmaf(s[2 * e + 1], p.scale_log2, -m));
+        const float a = ex2(far ? __fmul_rn(s[2 * e], p.scale_log2) - m
+                                : fmaf(s[2 * e], p.scale_log2, -m));
+        const float b = ex2(far ? __fmul_rn(s[2 * e + 1], p.scale_log2) - m
+                                : fmaf(s[2 * e + 1], p.scale_log2, -m));
         part[e & 1] = add2(part[e & 1], pair(a, b));
         u[e] = pack2<E>(a, b);
       }
@@ -605,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(misc + 640);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 644);
   int* s_n = reinterpret_cast<int*>(misc + 648);
-  // a result may hold what its row does not see
+  // a result may hold what its row does not see, or its scores are beyond kFar
   volatile int* redo = reinterpret_cast<volatile int*>(misc + 652);
   // [2]: the row tile's last step that its softmax warps made key by key
   volatile uint32_t* by_key = reinterpret_cast<volatile uint32_t*>(misc + 656);
@@ -1039,6 +1044,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f = factor(ref, now);
             ref = now;
             sum *= f;
+            if (valid && now != kNegInf && fabsf(now) >= kFar) *redo = 1;
             if (j > first) {
 #pragma unroll 1
               for (int i = 0; i < D; i += 16) {

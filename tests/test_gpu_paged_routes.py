@@ -225,3 +225,38 @@ def test_small_f16_weights_behind_a_dominant_key(lib, cuda_device, d, below):
             assert lib.gdn_device_status() == 0
             err = np.abs(o.double().cpu().numpy() - ref)
             assert (err <= bound).all(), float((err / ref).max())
+
+
+# ---- huge scores ------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("new,window", [((40,), 0), ((3,), 0), ((40,), 100)])
+def test_huge_scores(lib, cuda_device, dtype, new, window):
+    """Scores of some 10^11, whose rounding passes the exponentials' range: every
+    token takes its best key's value, and its score for the logarithm of the sum.
+
+    Bounds: fp32 scores are off by at most 128 2^-24 sum |q k| scale (the
+    tokens' two best scores are further apart, as is checked), so out is the
+    best key's value, to the bit, and lse is within that of the score."""
+    s = make(48, dtype=dtype, new=new, keys=(700,), poison=False, std=8000.0)
+    s["k_cache"] *= 8000.0
+    assert torch.isfinite(s["q"]).all() and torch.isfinite(s["k_cache"]).all()
+    place = torch.arange(700)
+    ids, rows = s["page_table"][0, place // 16].long(), place % 16
+    k, v = (s[n][ids, :, rows].double().repeat_interleave(2, 1)
+            for n in ("k_cache", "v_cache"))
+    q = s["q"][0].double()
+    score = torch.einsum("thd,khd->thk", q, k) * 64.0
+    off = torch.einsum("thd,khd->thk", q.abs(), k.abs()) * 64.0 * 128 * 2.0 ** -24
+    x = torch.arange(700 - new[0], 700)[:, None]
+    sees = (place <= x) & ((place > x - window) if window else (place >= 0))
+    score.masked_fill_(~sees[:, None], float("-inf"))
+    best = score.topk(2, -1)
+    assert (best.values[..., 0] - best.values[..., 1] > 4 * off.amax(-1)).all()
+    ref = torch.gather(v.transpose(0, 1), 1, best.indices[..., :1].transpose(0, 1)
+                       .expand(-1, -1, 128)).transpose(0, 1)
+    for t in tables(s):
+        for path in paths(lib):
+            o, lse = attend(lib, cuda_device, t, scale=64.0, window=window, path=path)
+            assert torch.equal(o[0].cpu().double(), ref)
+            err = (lse[0].cpu().double() - best.values[..., 0]).abs()
+            assert (err <= off.amax(-1) + 1e-6 * best.values[..., 0].abs()).all()
