@@ -648,18 +648,21 @@ def _paged_stream(stream, dev, tensors):
     marked as used on it, so that the allocator does not hand their memory out
     before the kernels are done with it. (The usual case, the current stream
     of the current device, has nothing to enter: these calls are short.)"""
+    # what may fail comes before the context is entered: callers leave it only
+    # if they have got it
     if stream is None:
+        raw = _raw_stream(dev.index)
         if _current_device() == dev.index:
-            return _raw_stream(dev.index), None
+            return raw, None
         ctx = torch.cuda.device(dev)
-        ctx.__enter__()
-        return _raw_stream(dev.index), ctx
-    ctx = torch.cuda.stream(stream)
+    else:
+        raw = stream.cuda_stream
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+        ctx = torch.cuda.stream(stream)
     ctx.__enter__()
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
-    return stream.cuda_stream, ctx
+    return raw, ctx
 
 
 def gdn_paged_append(q, k, v, k_cache, v_cache, page_table, kv_lens,

@@ -131,3 +131,37 @@ def test_packed_struct_matches_the_header(lib):
     assert len(raw) == ctypes.sizeof(C)
     c = C.from_buffer_copy(raw)
     assert [getattr(c, f[0]) for f in C._fields_] == list(range(1, 18))
+
+
+def test_a_failed_mark_leaves_the_stream_as_it_was(lib, monkeypatch):
+    """An input that cannot be marked as used on the given stream: the error
+    comes out and no stream context stays entered."""
+    from gated_deltanet_chunkwise_gb300 import abi
+    depth = []
+
+    class Context:
+        def __init__(self, *args):
+            pass
+
+        def __enter__(self):
+            depth.append(1)
+
+        def __exit__(self, *args):
+            depth.pop()
+
+    class Bad:
+        def record_stream(self, stream):
+            raise RuntimeError("no")
+
+    class Stream:
+        cuda_stream = 7
+
+    monkeypatch.setattr(torch.cuda, "stream", Context)
+    monkeypatch.setattr(torch.cuda, "device", Context)
+    with pytest.raises(RuntimeError, match="no"):
+        abi._paged_stream(Stream(), torch.device("cuda:0"), (None, Bad()))
+    assert not depth
+    raw, ctx = abi._paged_stream(Stream(), torch.device("cuda:0"), (None,))
+    assert raw == 7 and depth == [1]
+    ctx.__exit__(None, None, None)
+    assert not depth
