@@ -19,7 +19,8 @@ constexpr long long kMaxStride = 1ll << 38;
 bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s < kMaxStride; }
 
 int check_cache(const gdn_paged_cache_t* c, int B) {
-  if (!c || !c->k || !c->v || !c->page_table || !c->kv_lens)
+  // (arrays of no sequences have no address)
+  if (!c || !c->k || !c->v || (B > 0 && (!c->page_table || !c->kv_lens)))
     return GDN_ERR_INVALID_ARG;
   if (c->num_pages <= 0 || c->max_pages <= 0 || c->heads <= 0 ||
       c->table_stride < c->max_pages)

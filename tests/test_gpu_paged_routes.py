@@ -260,3 +260,19 @@ def test_huge_scores(lib, cuda_device, dtype, new, window):
             assert torch.equal(o[0].cpu().double(), ref)
             err = (lse[0].cpu().double() - best.values[..., 0]).abs()
             assert (err <= off.amax(-1) + 1e-6 * best.values[..., 0].abs()).all()
+
+
+def test_empty_batch(lib, cuda_device):
+    dev = cuda_device
+    s = make(49, new=(1,), keys=(20,))
+    kc, vc = s["k_cache"].to(dev), s["v_cache"].to(dev)
+    table = torch.empty((0, 4), dtype=torch.int32, device=dev)
+    lens = torch.empty((0,), dtype=torch.int32, device=dev)
+    q = torch.empty((0, 2, 4, 128), dtype=torch.bfloat16, device=dev)
+    for path in paths(lib):
+        o, lse = lib.gdn_paged_attn(q, kc, vc, table, lens, path=path,
+                                    return_lse=True)
+        assert o.shape == q.shape and lse.shape == q.shape[:3]
+    assert lib.gdn_paged_append(q, q[:, :, :2], q[:, :, :2], kc, vc, table,
+                                lens).shape == q.shape
+    assert lib.gdn_device_status() == 0

@@ -165,3 +165,12 @@ def test_a_failed_mark_leaves_the_stream_as_it_was(lib, monkeypatch):
     assert raw == 7 and depth == [1]
     ctx.__exit__(None, None, None)
     assert not depth
+
+
+def test_empty_batch(lib):
+    """A batch of no sequences has empty tensors, whose addresses are null."""
+    none = dict(B=0, table=0, lens=0, ts=4)
+    assert attn(lib, q=None, out=None, **none) == OK
+    assert append(lib, q=None, k=None, v=None, qo=None, **none) == OK
+    assert attn(lib, **dict(none, B=1)) == INVALID
+    assert append(lib, **dict(none, B=1)) == INVALID
