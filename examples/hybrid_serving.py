@@ -179,13 +179,15 @@ class HybridServer:
         return self._norm(x).float() @ self.embed.float().t()
 
 
-def serve(lengths=(70, 1, 200, 33), chunk=64, steps=12, seed=0, device="cuda"):
+def serve(lengths=(70, 1, 200, 33), chunk=64, steps=12, seed=0, device="cuda",
+          blocks=2):
     """Prefill in chunks and decode, then prefill everything at once; returns
     the decode steps' logits of both, [steps, requests, vocab]."""
     gen = torch.Generator(device=device)
     gen.manual_seed(seed + 1)
     most = max(lengths) + steps
-    server = HybridServer(len(lengths), most, device=device, seed=seed)
+    server = HybridServer(len(lengths), most, device=device, seed=seed,
+                          blocks=blocks)
     prompts = [torch.randint(server.vocab, (n,), generator=gen, device=device)
                for n in lengths]
     last = [None] * len(lengths)
@@ -202,7 +204,8 @@ def serve(lengths=(70, 1, 200, 33), chunk=64, steps=12, seed=0, device="cuda"):
         said.append(tokens)
         stepped.append(server.decode(tokens))
         tokens = stepped[-1].argmax(-1)
-    again = HybridServer(len(lengths), most, device=device, seed=seed)
+    again = HybridServer(len(lengths), most, device=device, seed=seed,
+                         blocks=blocks)
     whole = [torch.cat([p, torch.stack(said)[:, n]])
              for n, p in enumerate(prompts)]
     logits = again.prefill(whole)
