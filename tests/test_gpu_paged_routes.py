@@ -276,3 +276,158 @@ def test_empty_batch(lib, cuda_device):
     assert lib.gdn_paged_append(q, q[:, :, :2], q[:, :, :2], kc, vc, table,
                                 lens).shape == q.shape
     assert lib.gdn_device_status() == 0
+
+
+# ---- the cut list of the few-row kernel, and whatever else wide tables reach -----
+def check_wide(lib, dev, s, **kw):
+    t = tables(s)[1]
+    for path in paths(lib):
+        close(t, attend(lib, dev, t, path=path, **kw), **kw)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("keys", [1, 16, 63, 65, 129, 700, 3000])
+def test_wide_decode_lengths(lib, cuda_device, d, dtype, keys):
+    check_wide(lib, cuda_device, make(50, d=d, dtype=dtype, new=(1,), keys=(keys,)))
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("layout", ["hnd", "nhd", "joint"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_wide_pages_and_strides(lib, cuda_device, page, layout, dtype):
+    s = make(51, page=page, layout=layout, dtype=dtype, new=(3, 3), keys=(900, 131))
+    check_wide(lib, cuda_device, s)
+
+
+@pytest.mark.parametrize("window", [0, 1, 40, 1000])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new,keys", [((2, 2), (700, 90)), ((5, 5), (3, 0)),
+                                      ((70, 70), (200, 90))])
+def test_wide_masks(lib, cuda_device, window, causal, new, keys):
+    check_wide(lib, cuda_device, make(52, hq=6, hkv=2, new=new, keys=keys),
+               causal=causal, window=window)
+
+
+def test_wide_mix_of_few_and_many_rows(lib, cuda_device):
+    """Few rows on the average, some sequences with many, idle ones between: in
+    an automatic packed call each kernel takes its own."""
+    s = make(53, hq=2, hkv=1, new=(1, 2, 0, 70, 1, 1) + (1,) * 30,
+             keys=(50, 17, 9, 400, 1, 160) + tuple(range(3, 33)))
+    check_wide(lib, cuda_device, s)
+    s = make(53, hq=6, hkv=2, dtype="f16", new=(0, 1, 130, 0, 7, 33, 0),
+             keys=(50, 17, 400, 0, 7, 160, 3))
+    check_wide(lib, cuda_device, s)
+
+
+def test_wide_strided_queries(lib, cuda_device):
+    s = make(54, new=(3, 3), keys=(900, 60))
+    fused = torch.zeros(2, 3, 8, 128, dtype=torch.bfloat16)
+    fused[:, :, :4] = s["q"]
+    x = fused.to(cuda_device)
+    for t in tables(s):
+        args = [gpu(t[n], cuda_device) for n in ("k_cache", "v_cache", "page_table",
+                                                 "kv_lens")]
+        for path in paths(lib):
+            close(t, lib.gdn_paged_attn(x[:, :, :4], *args, path=path,
+                                        return_lse=True))
+
+
+@pytest.mark.parametrize("new,keys", [((1,) * 9, (900, 33, 512, 7, 64, 3000, 5, 300, 77)),
+                                      ((90,) * 3, (3000, 90, 500))])
+def test_same_bits_on_every_route(lib, cuda_device, new, keys):
+    """Twice, and on another stream, where pieces are joined through a workspace
+    and where they are not."""
+    s = make(55, new=new, keys=keys)
+    side = torch.cuda.Stream(cuda_device)
+    for t in tables(s):
+        for path in paths(lib):
+            a = attend(lib, cuda_device, t, path=path)
+            b = attend(lib, cuda_device, t, path=path)
+            side.wait_stream(torch.cuda.current_stream(cuda_device))
+            c = attend(lib, cuda_device, t, path=path, stream=side)
+            for x in (b, c):
+                assert torch.equal(a[0], x[0]) and torch.equal(a[1], x[1])
+
+
+def test_bad_lengths_and_pages_on_every_route(lib, cuda_device):
+    """A sequence whose keys do not fit its table is skipped, a page outside the
+    pool reads as zeros; the others are right."""
+    dev = cuda_device
+    for new in ((1, 1), (40, 40)):
+        s = make(56, new=new, keys=(140, 160))
+        ref, _, mag = paged.attend(s["q"], s["k_cache"], s["v_cache"],
+                                   s["page_table"], s["kv_lens"])
+        for t in tables(s):
+            width = t["page_table"].shape[1]
+            for path in paths(lib):
+                def run(table, lens):
+                    out = torch.full(t["q"].shape, 7.0, dtype=torch.bfloat16,
+                                     device=dev)
+                    lib.gdn_paged_attn(t["q"].to(dev), t["k_cache"].to(dev),
+                                       t["v_cache"].to(dev), table.to(dev),
+                                       lens.to(dev), out=out, path=path)
+                    assert lib.gdn_device_status() == -1
+                    return out.float().cpu().numpy()
+
+                for bad in (-1, 16 * width + 1):
+                    lens = t["kv_lens"].clone()
+                    lens[0] = bad
+                    o = run(t["page_table"], lens)
+                    assert (o[0] == 7.0).all()
+                    assert (np.abs(o[1] - ref[1]) <= 2 ** -6 * mag[1] + 1e-30).all()
+                for bad in (-1, t["k_cache"].shape[0]):
+                    table = t["page_table"].clone()
+                    table[0, 1] = bad
+                    o = run(table, t["kv_lens"])
+                    assert np.isfinite(o[0]).all()
+                    assert (np.abs(o[1] - ref[1]) <= 2 ** -6 * mag[1] + 1e-30).all()
+
+
+# ---- graphs -------------------------------------------------------------------------
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("new", [1, 2, 40])
+def test_every_route_in_a_graph(lib, cuda_device, wide, new):
+    """Append and attention captured once and replayed as the sequences grow, on
+    each kernel: workspace, cut list, joined pieces and all."""
+    dev = cuda_device
+    s = make(57, page=64, new=(new,) * 3, keys=(new + 14, new + 31, new + 800),
+             poison=False)
+    # a page more for each to grow into (of a pool of its own)
+    pages = [-(-int(k) // 64) + 1 for k in s["kv_lens"]]
+    table = torch.full((3, 200 if wide else max(pages)), -7, dtype=torch.int32)
+    order = torch.randperm(sum(pages), generator=torch.Generator().manual_seed(1))
+    for i, n in enumerate(pages):
+        table[i, :n] = order[sum(pages[:i]):sum(pages[:i]) + n].to(torch.int32)
+    shape = (sum(pages),) + s["k_cache"].shape[1:]
+    kc, vc = s["normal"](shape).to(dev), s["normal"](shape).to(dev)
+    rope = table_of(1100, 128).to(dev)
+    table, lens = table.to(dev), s["kv_lens"].to(dev)
+    x = s["normal"]((3, new, 8, 128)).to(dev)
+    for path in paths(lib):
+        def step():
+            q = lib.gdn_paged_append(x[:, :, :4], x[:, :, 4:6], x[:, :, 6:], kc,
+                                     vc, table, lens, rope=rope)
+            return lib.gdn_paged_attn(q, kc, vc, table, lens, return_lse=True,
+                                      path=path)
+
+        lens.copy_(s["kv_lens"])
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        for _ in range(3):
+            lens += 1 if new == 1 else 7
+            x.copy_(s["normal"]((3, new, 8, 128)))
+            graph.replay()
+            torch.cuda.synchronize()
+            got = [t.clone() for t in out]
+            want = step()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+            ref, rl, mag = paged.attend(
+                lib.gdn_paged_append(x[:, :, :4], x[:, :, 4:6], x[:, :, 6:], kc, vc,
+                                     table, lens, rope=rope), kc, vc, table, lens)
+            err = np.abs(got[0].double().cpu().numpy() - ref)
+            assert (err <= 2.0 ** -8 * (np.abs(ref) + 1.02 * mag) + 4e-4 * mag).all()
+    assert lib.gdn_device_status() == 0
