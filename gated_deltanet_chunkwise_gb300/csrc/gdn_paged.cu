@@ -167,12 +167,16 @@ extern "C" int gdn_paged_attn(const void* q, int64_t q_stride,
   // paged_rows.cu, more go to the tensor-core tiles (32 sequences of 4096
   // keys, 4 key heads: 16 rows 58.6 us against 64.5 us, 24 rows, a second
   // block of them, 80 us against 65 us; 64-wide heads 37 against 53 and 56
-  // against 54). A packed batch of few rows on the average may hold longer
-  // sequences all the same: each kernel takes its own. A call that the few-row
-  // kernel splits (a short cache) goes there with any number of rows: one
-  // launch and no tensor-core tiles to fill (one user, 5 tokens of 32 heads, 4
-  // key heads, 1024 keys 10 us against 15, 32 tokens 13 against 19; 128 tokens,
-  // 512 keys 14 against 19).
+  // against 54; sequences alike). A packed batch of few rows on the average may
+  // hold longer sequences all the same: each kernel takes its own (127 single
+  // tokens after 500 to 2000 keys and a prompt of 300, 32 heads, 8 key heads:
+  // 142 us, 175 on the tiles, 139 in two calls). One of many rows on the average
+  // takes the tiles for its single tokens, too (63 after 500 to 4000 keys and a
+  // chunk of 2048: 179 us, 170 in two calls; 31 after 200 to 1000 and 1024: 56
+  // us, 63 in two calls). A call that the few-row kernel splits (a short cache)
+  // goes there with any number of rows: one launch and no tensor-core tiles to
+  // fill (one user, 5 tokens of 32 heads, 4 key heads, 1024 keys 10 us against
+  // 15, 32 tokens 13 against 19; 128 tokens, 512 keys 14 against 19).
   const int split = path == GDN_PAGED_TILES ? 0 : paged_rows_split(p);
   const long long mean = (long long)T * p.group;  // rows (packed: times B)
   const bool few = mean <= 16ll * (cu_seqlens ? B : 1);

@@ -49,13 +49,21 @@ constexpr int kThreads = (kConsumers + 1) * 32;
 constexpr int ROWS = 16;     // rows per block
 constexpr int kCtasPerSm = 2;
 // Split calls: up to 8 CTAs an item, where the table holds up to 512 keys for
-// each of them. One user, 8 key heads, D = 128, us in a graph and (one call
-// after the other, bound by the host) split against cut: 64 keys 6.3 (16)
-// against 7.5 (22), 1024 9.9 (16) against 9.9 (22), 4096 14.1 (16) against 11.9
-// (22), 8192 20 (20) against 14 (22); 32 users, one CTA an item: 512 keys 17
-// against 22.
+// each of them; 320 where single tokens leave a quarter of the CTAs idle, which
+// the even cut would use. (More rows than one block go to the tiles otherwise:
+// 40 rows, 4 key heads, 4096 keys 14.5 us against 23.8.) Single tokens, 8 key
+// heads, D = 128, us in a graph and (one call after the other, where the cut's
+// second launch and workspace show on the host) split against cut:
+//   one user     64 keys 5.8 (10.1) against 7.1 (13.4), 2048 11.2 (11.3) against
+//                10.2 (14.0), 3072 12.5 (12.7) against 10.7 (14.6), 4096 14.0
+//                (14.2) against 11.0 (14.6)
+//   two users    2048 keys 12.3 (12.5) against 10.4 (15.3), 3072 13.8 (13.9)
+//                against 11.2 (13.6)
+//   four users   (256 of 304 CTAs) 4096 keys 16.1 (16.3) against 16.7 (16.8)
+//   32 users     (one CTA an item) 512 keys 12.4 (12.7) against 16.8 (17.1)
 constexpr int kMaxSplit = 8;
 constexpr int kSplitKeys = 512;
+constexpr int kSplitKeysIdle = 320;
 
 template <int D>
 struct Shape {
@@ -818,9 +826,13 @@ int paged_rows_box(int page_size) { return page_size < TK ? page_size : TK; }
 
 int paged_rows_split(const PagedAttnParams& p) {
   const long long keys = (long long)p.c.max_pages << p.c.page_shift;
-  for (int s = kMaxSplit; s > 0; s /= 2)
-    if (item_bound(p) * s <= rows_grid() && (s == 1 || keys > TK * (s / 2)))
-      return keys <= (long long)kSplitKeys * s ? s : 0;
+  const bool few = (long long)p.T * p.group <= (long long)ROWS * (p.cu ? p.N : 1);
+  for (int s = kMaxSplit; s > 0; s /= 2) {
+    const long long ctas = item_bound(p) * s;
+    if (ctas > rows_grid() || (s > 1 && keys <= TK * (s / 2))) continue;
+    const bool idle = few && 4 * ctas < 3ll * rows_grid();
+    return keys <= (long long)(idle ? kSplitKeysIdle : kSplitKeys) * s ? s : 0;
+  }
   return 0;
 }
 

@@ -431,3 +431,24 @@ def test_every_route_in_a_graph(lib, cuda_device, wide, new):
             err = np.abs(got[0].double().cpu().numpy() - ref)
             assert (err <= 2.0 ** -8 * (np.abs(ref) + 1.02 * mag) + 4e-4 * mag).all()
     assert lib.gdn_device_status() == 0
+
+
+# ---- the few-row kernel's choice ------------------------------------------------------
+@pytest.mark.parametrize("tokens,users,keys,launches", [
+    (1, 1, 2560, 1), (1, 1, 2576, 2), (1, 1, 4096, 2),   # CTAs idle: to 320 each
+    (1, 4, 4096, 1), (1, 4, 4112, 2),                    # few idle: to 512 each
+    (5, 1, 4096, 1), (5, 1, 4112, 2)])                   # or the tiles
+def test_which_calls_are_split(lib, cuda_device, tokens, users, keys, launches):
+    """Short tables take one launch, longer ones a second that joins pieces: by
+    what the table can hold, the CTAs left over and the rows."""
+    dev = cuda_device
+    if torch.cuda.get_device_properties(dev).multi_processor_count != 152:
+        pytest.skip("the limits below are those of 152 SMs")
+    s = make(58, hq=32, hkv=8, new=(tokens,) * users, keys=(30,) * users)
+    table = torch.full((users, keys // 16), -7, dtype=torch.int32)
+    table[:, :2] = s["page_table"][:, :2]
+    t = dict(s, page_table=table)
+    before = lib.kernel_counters()
+    got = attend(lib, dev, t)
+    assert lib.kernel_counters() - before == launches
+    close(t, got)
