@@ -366,27 +366,27 @@ __device__ __forceinline__ void serve(const PagedAttnParams& p,
       uint32_t qf[KS][4];
       int hi[2], lo[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = h * 8 + g8;
-          const int row = g.block * ROWS + min(r, nrows - 1);
-          const int tok = row / p.group;
-          const int x = walk.s.kv - walk.s.len + tok;
-          hi[h] = p.causal ? min(x + 1, walk.s.kv) : walk.s.kv;
-          lo[h] = p.window > 0 ? max(0, x - p.window + 1) : 0;
-          const E* q = static_cast<const E*>(p.q) +
-                       (walk.s.q0 + (long long)tok) * p.q_row +
-                       (long long)(g.head * p.group + row % p.group) * D;
+      for (int h = 0; h < 2; ++h) {
+        const int r = h * 8 + g8;
+        const int row = g.block * ROWS + min(r, nrows - 1);
+        const int tok = row / p.group;
+        const int x = walk.s.kv - walk.s.len + tok;
+        hi[h] = p.causal ? min(x + 1, walk.s.kv) : walk.s.kv;
+        lo[h] = p.window > 0 ? max(0, x - p.window + 1) : 0;
+        const E* q = static_cast<const E*>(p.q) +
+                     (walk.s.q0 + (long long)tok) * p.q_row +
+                     (long long)(g.head * p.group + row % p.group) * D;
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            qf[ks][h] = qf[ks][2 + h] = 0u;
-            if (r < nrows) {
-              qf[ks][h] =
-                  *reinterpret_cast<const uint32_t*>(q + ks * 16 + 2 * t4);
-              qf[ks][2 + h] =
-                  *reinterpret_cast<const uint32_t*>(q + ks * 16 + 8 + 2 * t4);
-            }
+        for (int ks = 0; ks < KS; ++ks) {
+          qf[ks][h] = qf[ks][2 + h] = 0u;
+          if (r < nrows) {
+            qf[ks][h] =
+                *reinterpret_cast<const uint32_t*>(q + ks * 16 + 2 * t4);
+            qf[ks][2 + h] =
+                *reinterpret_cast<const uint32_t*>(q + ks * 16 + 8 + 2 * t4);
           }
         }
+      }
       // keys [free_lo, free_hi) are seen by every row of the block; keys
       // outside [any_lo, kv) by none
       const int x0 = walk.s.kv - walk.s.len + g.block * ROWS / p.group;
@@ -400,11 +400,11 @@ __device__ __forceinline__ void serve(const PagedAttnParams& p,
 
       float acc[D / 8][4];
       float mx[2], sum[2];
-        mx[0] = mx[1] = kNegInf;
-        sum[0] = sum[1] = 0.f;
+      mx[0] = mx[1] = kNegInf;
+      sum[0] = sum[1] = 0.f;
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j)
-          acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+      for (int j = 0; j < D / 8; ++j)
+        acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
 
       for (int t = g.t0; ok && t < g.t1; ++t, ++it) {
         const int st = it % S::kStages;
@@ -429,60 +429,60 @@ __device__ __forceinline__ void serve(const PagedAttnParams& p,
           }
           float s[2][4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-              s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+          for (int j = 0; j < 2; ++j)
+            s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
           const uint32_t ka = smem_u32(ks_), va = smem_u32(vs_);
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
             uint32_t bfr[4];
             ldsm4(ka + tile_off(kb + (mat >> 1) * 8 + r8, 2 * ks + (mat & 1)),
                   bfr);
-              mma16816(s[0], qf[ks], bfr[0], bfr[1], E());
-              mma16816(s[1], qf[ks], bfr[2], bfr[3], E());
+            mma16816(s[0], qf[ks], bfr[0], bfr[1], E());
+            mma16816(s[1], qf[ks], bfr[2], bfr[3], E());
           }
           const bool masked = key0 < free_lo || key0 + 16 > free_hi;
           bool grow = false;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float x = __fmul_rn(s[j][e], p.scale_log2);  // (see kFar)
-                if (masked) {
-                  const int key = key0 + j * 8 + 2 * t4 + (e & 1);
-                  if (key >= hi[e >> 1] || key < lo[e >> 1]) x = kNegInf;
-                }
-                s[j][e] = x;
-                grow = grow || !(x <= mx[e >> 1] + kSlack + kLift<E>);  // (NaN too)
+            for (int e = 0; e < 4; ++e) {
+              float x = __fmul_rn(s[j][e], p.scale_log2);  // (see kFar)
+              if (masked) {
+                const int key = key0 + j * 8 + 2 * t4 + (e & 1);
+                if (key >= hi[e >> 1] || key < lo[e >> 1]) x = kNegInf;
               }
+              s[j][e] = x;
+              grow = grow || !(x <= mx[e >> 1] + kSlack + kLift<E>);  // (NaN too)
+            }
           if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float top = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]),
-                                  fmaxf(s[1][2 * h], s[1][2 * h + 1]));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float now = fmaxf(mx[h], top - kLift<E>);
-                const float f = factor(mx[h], now);
-                mx[h] = now;
-                sum[h] *= f;
+            for (int h = 0; h < 2; ++h) {
+              float top = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]),
+                                fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+              const float now = fmaxf(mx[h], top - kLift<E>);
+              const float f = factor(mx[h], now);
+              mx[h] = now;
+              sum[h] *= f;
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                  acc[j][2 * h] *= f;
-                  acc[j][2 * h + 1] *= f;
-                }
+              for (int j = 0; j < D / 8; ++j) {
+                acc[j][2 * h] *= f;
+                acc[j][2 * h + 1] *= f;
               }
+            }
           }
           uint32_t pf[4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float ref = mx[h] == kNegInf ? 0.f : mx[h];
-                const float a = ex2(s[j][2 * h] - ref);
-                const float b = ex2(s[j][2 * h + 1] - ref);
-                sum[h] += a + b;
-                pf[2 * j + h] = pack2<E>(a, b);
-              }
+            for (int h = 0; h < 2; ++h) {
+              const float ref = mx[h] == kNegInf ? 0.f : mx[h];
+              const float a = ex2(s[j][2 * h] - ref);
+              const float b = ex2(s[j][2 * h + 1] - ref);
+              sum[h] += a + b;
+              pf[2 * j + h] = pack2<E>(a, b);
+            }
           bool by_key = false;
           if (CAREFUL && masked) {
             // look through the values of the warp's keys
@@ -539,38 +539,38 @@ __device__ __forceinline__ void serve(const PagedAttnParams& p,
 
       // ---- join the four warps -------------------------------------------------
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float l = sum[h];
-          l += __shfl_xor_sync(0xffffffffu, l, 1);
-          l += __shfl_xor_sync(0xffffffffu, l, 2);
-          if (t4 == 0) {
-            c.m[warp][h * 8 + g8] = mx[h];
-            c.l[warp][h * 8 + g8] = l;
-          }
+      for (int h = 0; h < 2; ++h) {
+        float l = sum[h];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        if (t4 == 0) {
+          c.m[warp][h * 8 + g8] = mx[h];
+          c.l[warp][h * 8 + g8] = l;
         }
+      }
       named_bar(1, kConsumers * 32);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = h * 8 + g8;
-          float top = kNegInf;
+      for (int h = 0; h < 2; ++h) {
+        const int r = h * 8 + g8;
+        float top = kNegInf;
 #pragma unroll
-          for (int w = 0; w < kConsumers; ++w)
-            top = fmaxf(top, c.m[w][r]);
-          float l = 0.f;
+        for (int w = 0; w < kConsumers; ++w)
+          top = fmaxf(top, c.m[w][r]);
+        float l = 0.f;
 #pragma unroll
-          for (int w = 0; w < kConsumers; ++w)
-            l += c.l[w][r] * factor(c.m[w][r], top);
-          const float f = factor(mx[h], top);
+        for (int w = 0; w < kConsumers; ++w)
+          l += c.l[w][r] * factor(c.m[w][r], top);
+        const float f = factor(mx[h], top);
 #pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            acc[j][2 * h] *= f;
-            acc[j][2 * h + 1] *= f;
-          }
-          if (warp == 0 && t4 == 0) {
-            c.M[r] = top;
-            c.L[r] = l;
-          }
+        for (int j = 0; j < D / 8; ++j) {
+          acc[j][2 * h] *= f;
+          acc[j][2 * h + 1] *= f;
         }
+        if (warp == 0 && t4 == 0) {
+          c.M[r] = top;
+          c.L[r] = l;
+        }
+      }
       // turns: 3 -> 2, 1 -> (after) 0, 2 -> 0 through one buffer, in a fixed
       // order
 #pragma unroll 1
