@@ -18,6 +18,19 @@ constexpr long long kMaxStride = 1ll << 38;
 
 bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s < kMaxStride; }
 
+// Whether rows of `wa` elements `sa` apart from a on and rows of `wb` elements
+// `sb` apart from b on share memory (both 16-bit, `rows` of each; yes, too, where
+// their strides differ and only their ends lie apart).
+bool rows_overlap(const void* a, int64_t sa, int64_t wa, const void* b,
+                  int64_t sb, int64_t wb, long long rows) {
+  const auto x = static_cast<long long>(reinterpret_cast<uintptr_t>(a) / 2);
+  const auto y = static_cast<long long>(reinterpret_cast<uintptr_t>(b) / 2);
+  if (x + (rows - 1) * sa + wa <= y || y + (rows - 1) * sb + wb <= x) return false;
+  if (sa != sb) return true;
+  const long long off = ((y - x) % sa + sa) % sa;
+  return off < wa || off + wb > sa;
+}
+
 int check_cache(const gdn_paged_cache_t* c, int B) {
   // (arrays of no sequences have no address)
   if (!c || !c->k || !c->v || (B > 0 && (!c->page_table || !c->kv_lens)))
@@ -112,12 +125,17 @@ extern "C" int gdn_paged_append(
             q_stride < (int64_t)Hq * cache->d ||
             q_out_stride < (int64_t)Hq * cache->d))
     return GDN_ERR_INVALID_ARG;
-  // in place only row for row
-  if (q && q == q_out && q_stride != q_out_stride) return GDN_ERR_INVALID_ARG;
   const void* ptrs[] = {q, k, v, q_out, rope};
   for (const void* x : ptrs)
     if (x && !aligned(x, 16)) return GDN_ERR_MISALIGNED;
   if (positions && !aligned(positions, 4)) return GDN_ERR_MISALIGNED;
+  // in place only row for row
+  const int64_t wq = (int64_t)Hq * cache->d, wkv = (int64_t)cache->heads * cache->d;
+  if (q && ((!(q == q_out && q_stride == q_out_stride) &&
+             rows_overlap(q, q_stride, wq, q_out, q_out_stride, wq, tokens)) ||
+            rows_overlap(k, k_stride, wkv, q_out, q_out_stride, wq, tokens) ||
+            rows_overlap(v, v_stride, wkv, q_out, q_out_stride, wq, tokens)))
+    return GDN_ERR_INVALID_ARG;
   if ((rc = device_status_ptr(&p.status)) != GDN_OK) return rc;
   p.c = view(cache);
   p.q = q; p.k = k; p.v = v; p.q_out = q_out;
@@ -149,11 +167,14 @@ extern "C" int gdn_paged_attn(const void* q, int64_t q_stride,
   if (Hq / cache->heads > 128) return GDN_ERR_UNSUPPORTED;
   const long long tokens = cu_seqlens ? (long long)T : (long long)B * T;
   if (tokens == 0) return GDN_OK;
-  if (!q || !out || out == q) return GDN_ERR_INVALID_ARG;
+  if (!q || !out) return GDN_ERR_INVALID_ARG;
   if (!stride_ok(q_stride) || q_stride < (int64_t)Hq * cache->d)
     return GDN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4))
     return GDN_ERR_MISALIGNED;
+  const int64_t wq = (int64_t)Hq * cache->d;
+  if (rows_overlap(q, q_stride, wq, out, wq, wq, tokens))
+    return GDN_ERR_INVALID_ARG;
   PagedAttnParams p{};
   if ((rc = device_status_ptr(&p.status)) != GDN_OK) return rc;
   p.c = view(cache);

@@ -449,7 +449,8 @@ typedef struct {
  *               tokens q_stride / k_stride / v_stride elements apart (a
  *               multiple of 8, >= H d: slices of one fused projection work),
  *               heads contiguous; q may be NULL (keys and values only)
- *   q_out       like q, q_out_stride apart; may be q itself
+ *   q_out       like q, q_out_stride apart; may be q itself, but share no
+ *               other memory with q, k or v
  *   rope        fp32 [rope_rows, rot]: row p holds cos, then sin, of position
  *               p's rot/2 angles; NULL with rot = 0: no rotation
  *   rot         rotated elements of a head: a multiple of 16, <= d. Pair i is
@@ -506,7 +507,7 @@ int gdn_paged_append(const void* q, int64_t q_stride, const void* k,
  *               kv_lens[n] keys
  *   window      0, or > 0: keys x - window and before are not seen; pages
  *               that lie wholly there are never read
- *   out         16-bit [B, T, Hq, d] contiguous (written); not q
+ *   out         16-bit [B, T, Hq, d] contiguous (written); no memory of q
  *   lse         fp32 [B, T, Hq] or NULL: natural log of the sum of exponentials
  *   path        GDN_PAGED_*
  * A token that sees no key (more new tokens than keys) gets out = 0 and lse =
@@ -516,10 +517,13 @@ int gdn_paged_append(const void* q, int64_t q_stride, const void* k,
  * reaches the tokens that see it and no others. Scores, maxima, sums and
  * accumulators are fp32; weights are rounded to the 16-bit type for their
  * product with V (fp16: to 11 bits down to 2^-21 of a row's largest one, to
- * multiples of 2^-31 of it below), and the output once. A sequence whose keys do not fit the
- * table is skipped (its rows are not written), offsets that decrease or leave
- * [0, T] leave every row unwritten, and a page outside the pool reads as zeros;
- * all three record GDN_ERR_INVALID_ARG. Results do not depend on timing.
+ * multiples of 2^-31 of it below), and the output once. A sequence whose keys
+ * do not fit the table is skipped (its rows are not written), offsets that
+ * decrease or leave [0, T] leave every row unwritten, and a page outside the
+ * pool reads as zeros; all three record GDN_ERR_INVALID_ARG. Results do not
+ * depend on timing. (A call in which values that are not finite are seen by
+ * some tokens of a tile and hidden from others, or scores pass 2^20, takes some
+ * times longer.)
  * Workspace: none (a table of few pages), 5 MB (few rows) or up to 41 MB per
  * call in flight, stream-ordered, from a memory pool of the library's own on
  * the device that keeps what it has been given (the device's default pool would

@@ -174,3 +174,35 @@ def test_empty_batch(lib):
     assert append(lib, q=None, k=None, v=None, qo=None, **none) == OK
     assert attn(lib, **dict(none, B=1)) == INVALID
     assert append(lib, **dict(none, B=1)) == INVALID
+
+
+@pytest.mark.parametrize("kw,expect", [
+    # 5 tokens of 4 heads of 128: 5120 bytes each, one after the other or apart
+    (dict(T=5, out=A + 16), INVALID), (dict(T=5, out=A - 16), INVALID),
+    (dict(T=5, out=A + 5104), INVALID), (dict(T=5, out=A - 5104), INVALID),
+    (dict(T=5, qs=1024, out=A + 9200), INVALID),
+    (dict(T=0, out=A), OK),
+])
+def test_output_over_the_queries(lib, kw, expect):
+    """An output that lies over part of the queries would be written while other
+    blocks still read them."""
+    assert attn(lib, **kw) == expect
+
+
+@pytest.mark.parametrize("kw,expect", [
+    # fused rows of 8 heads of 128: 4 of queries, 2 of keys, 2 of values
+    (dict(qo=A + 2 * 512), INVALID),                  # over the keys
+    (dict(qo=A + 2 * 128), INVALID),                  # half over the queries
+    (dict(qo=A - 2 * 128), INVALID),                  # and over the last values
+    (dict(qo=A + 2 * 1024), INVALID),                 # a row further
+    (dict(qo=A, qos=512), INVALID), (dict(qo=A + 64, qos=512), INVALID),
+    (dict(T=0, qo=A + 2 * 128), OK),
+])
+def test_append_output_over_the_inputs(lib, kw, expect):
+    f = dict(T=5, q=A, qs=1024, k=A + 2 * 512, ks=1024, v=A + 2 * 768, vs=1024,
+             qos=1024)
+    assert append(lib, **dict(f, **kw)) == expect
+    # in place, or beside them: past the checks (and no further without a GPU)
+    for qo, qos in ((A, 1024), (A + (1 << 20), 512)):
+        if not torch.cuda.is_available():
+            assert append(lib, **dict(f, qo=qo, qos=qos)) not in (INVALID, UNSUPPORTED)
