@@ -18,8 +18,9 @@
 // vectors of a head (the two halves of 8 pairs) and walks over the heads with
 // the cosines and sines of its pairs in registers, so the table is read once
 // per token and lane, not once per head. Three head rows are loaded before the
-// first is stored: 15,100 tokens of 32 + 2 * 8 heads of 128 (379 MB) take
-// 62 us by events around the launch, 6.1 TB/s (two rows 68 us, six 63 us).
+// first is stored: 15,100 tokens of 32 + 2 * 8 heads of 128 (379 MB) take 58 us
+// a call one after the other, 6.5 TB/s (between events around each launch, which
+// add 4 us: 62 us, two rows 68 us, six 63 us).
 #include "paged.cuh"
 
 namespace gdn {

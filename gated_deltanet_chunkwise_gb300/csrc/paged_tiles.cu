@@ -23,16 +23,15 @@
 //
 // The reference m (for fp16 2^7 below the maximum) follows the running maximum
 // only when a score passes it by more than 2^8 (weights stay below 2^8, fp16
-// ones below 2^15; sums and O are fp32), so O, which
-// lives in TMEM, is rarely rescaled, and the softmax warps do it themselves:
-// S(j + 1)'s barrier already says that O += P(j) V(j) is complete. Weights are
-// rounded to 16 bits for their product (2^-9 on the average, as the output
-// is); sums take them unrounded.
+// ones below 2^15; sums and O are fp32), so O, which lives in TMEM, is rarely
+// rescaled, and the softmax warps do it themselves: S(j + 1)'s barrier already
+// says that O += P(j) V(j) is complete. Weights are rounded to 16 bits for their
+// product (2^-9 on the average, as the output is); sums take them unrounded.
 //
 // Bound: the tensor core, 4 D flops a visible (row, key) pair: 2048 tokens of
-// 16 heads against 65536 keys, D = 128 (1.08 TFLOP) take 671 us, 1.6 PFLOP/s,
-// and 716 us called over and over (power-capped). Of a step's 3100 cycles the
-// products take 2340. The exponentials (one a pair, 32 a cycle and SM) take
+// 16 heads against 65536 keys, D = 128 (1.08 TFLOP) take 672 us, 1.6 PFLOP/s,
+// and 720 to 740 us called over and over (power-capped). Of a step's 2850 cycles
+// the products take 2340. The exponentials (one a pair, 32 a cycle and SM) take
 // 1024 beside them. Short items are bound by what they cost once: 3 us to find
 // a run's place and 4 us to the first scores, 2 us a change of item, 3 us for
 // the last one's output.
