@@ -967,6 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int free_lo = p.window > 0 ? x0 + g.ntok[t] - p.window : 0;
         const int any_lo = g.lo, any_hi = g.hi;
         const int s0 = g.s0, first = g.first[t], last = g.last[t];
+        const int looks = g.first[1 - t] < g.last[1 - t] ? 8 : 0;
         float ref = kNegInf, sum = 0.f;
         int begin = first;
         if (g.careful) {
@@ -995,13 +996,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(t_s, x[0]);
           tmem_ld32(t_s + 32, x[1]);
           // Let the other row tile's warp of this scheduler finish its first
-          // half (some 40 cycles a look, and then on in any case: it may have no
-          // such step). The row tiles fall into step with each other otherwise:
-          // their exponentials share the scheduler, then the tensor core waits
-          // (2048 tokens over 65536 keys 725 us, 880 without the looks; before
-          // masked tiles they cost more than they give).
+          // half (some 40 cycles a look, and then on in any case). The row tiles
+          // fall into step with each other otherwise: their exponentials share
+          // the scheduler, then the tensor core waits (2048 tokens over 65536
+          // keys 725 us, 880 without the looks). Not before masked tiles, where
+          // looks cost more than they give, nor where the other row tile has no
+          // keys (4 drafted tokens of 8 heads over 3000 to 9000 keys, D = 64:
+          // 39.8 us, 41.0 with).
 #pragma unroll 1
-          for (int i = 0; !masked && i < 8 && busy[warp ^ 4] != 0; ++i) {
+          for (int i = 0; !masked && i < looks && busy[warp ^ 4] != 0; ++i) {
           }
           __syncwarp();
           if (lane == 0) busy[warp] = 1;
